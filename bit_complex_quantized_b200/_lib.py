@@ -19,6 +19,8 @@ IFQ_MAX_GROUP = 32
 IFQ_QUANT_STATIC_SCRATCH_BYTES = 2 << 20
 IFQ_DEV_NONFINITE = 0x1
 IFQ_DEV_TIMEOUT = 0x2
+IFQ_DEV_RANGE = 0x4
+IFQ_KV4_MAX_NEW = 16
 
 EXPORTED = (
     "ifq_status_string",
@@ -38,6 +40,13 @@ EXPORTED = (
     "ifq_gemv_run",
     "ifq_gemm",
     "ifq_gemm_wait_limit",
+    "ifq_w4_quantize",
+    "ifq_w4_dequantize",
+    "ifq_w4_gemv",
+    "ifq_kv4_append",
+    "ifq_kv4_read",
+    "ifq_kv4_attention_workspace_bytes",
+    "ifq_kv4_attention",
 )
 
 STATUS_NAMES = {
@@ -80,6 +89,29 @@ class Layer(ctypes.Structure):
                 ("scales_w", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("x_re", ctypes.c_void_p), ("x_im", ctypes.c_void_p), ("y_re", ctypes.c_void_p),
                 ("y_im", ctypes.c_void_p), ("rot_re", ctypes.c_void_p), ("rot_im", ctypes.c_void_p)]
+
+
+class W4Tensor(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class W4DqTensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("w", ctypes.c_void_p)]
+
+
+class W4Layer(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("x_re", ctypes.c_void_p), ("x_im", ctypes.c_void_p),
+                ("y_re", ctypes.c_void_p), ("y_im", ctypes.c_void_p)]
+
+
+class Kv4CacheDesc(ctypes.Structure):
+    _fields_ = [("records", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("n_new", ctypes.c_int32), ("rows", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("table_cols", ctypes.c_int64), ("kv_lens", ctypes.c_void_p), ("new_offsets", ctypes.c_void_p)]
 
 
 _lib = None
@@ -128,6 +160,21 @@ def load():
     lib.ifq_gemm.argtypes = [ctypes.POINTER(Layer), i32, i32, i64, vp, vp]
     lib.ifq_gemm_wait_limit.restype = i32
     lib.ifq_gemm_wait_limit.argtypes = [ctypes.POINTER(Layer), i32, i32, i64, ctypes.c_uint64, vp, vp]
+    lib.ifq_w4_quantize.restype = i32
+    lib.ifq_w4_quantize.argtypes = [ctypes.POINTER(W4Tensor), i32, i32, vp, vp]
+    lib.ifq_w4_dequantize.restype = i32
+    lib.ifq_w4_dequantize.argtypes = [ctypes.POINTER(W4DqTensor), i32, i32, vp]
+    lib.ifq_w4_gemv.restype = i32
+    lib.ifq_w4_gemv.argtypes = [ctypes.POINTER(W4Layer), i32, i32, i32, vp, vp]
+    kvp = ctypes.POINTER(Kv4CacheDesc)
+    lib.ifq_kv4_append.restype = i32
+    lib.ifq_kv4_append.argtypes = [kvp, vp, vp, vp, vp, i64, vp, vp]
+    lib.ifq_kv4_read.restype = i32
+    lib.ifq_kv4_read.argtypes = [kvp, vp, vp, vp, vp, i64, vp, vp]
+    lib.ifq_kv4_attention_workspace_bytes.restype = sz
+    lib.ifq_kv4_attention_workspace_bytes.argtypes = [kvp, i32]
+    lib.ifq_kv4_attention.restype = i32
+    lib.ifq_kv4_attention.argtypes = [kvp, i32, vp, vp, i64, ctypes.c_float, vp, vp, i64, vp, sz, vp, vp]
     _lib = lib
     return lib
 
@@ -314,6 +361,164 @@ def ifq_gemm_wait_limit(layers, T, M, wait_limit_ns, dev_status=None, stream=Non
     """As ifq_gemm with each pipeline wait bounded by wait_limit_ns (IFQ_DEV_TIMEOUT when one runs out)."""
     arr, n = _as_array(layers)
     _check(load().ifq_gemm_wait_limit(arr, n, T, M, int(wait_limit_ns), _ptr(dev_status), _stream(stream)))
+
+
+# ------------------------------------------------------------------ 4-bit layers and cache
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _device_of(tensors):
+    """The one CUDA device of all given tensors (None entries are skipped)."""
+    devs = {t.device for t in tensors if t is not None}
+    _need(len(devs) == 1 and next(iter(devs)).type == "cuda", "all tensors of a call must be on one CUDA device")
+    return next(iter(devs))
+
+
+def _enqueue(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current; stream: that device's current one by default."""
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(stream)))
+
+
+def _plane(t, shape, dtype, what):
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    _need(t.dtype in dtypes and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{what}: needs a contiguous {dtypes[0]} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values or their bit patterns
+
+
+def w4_shapes(rows, cols, group):
+    """Shapes of the codes (uint8) and scales (bf16) of a 4-bit [rows][cols] layer."""
+    return ((rows + 15) // 16, cols // 64, 512), ((rows + 15) // 16, cols // group, 16)
+
+
+def _w4_buffers(codes, scales, rows, cols, group):
+    _need(group in (32, 64, 128) and cols > 0 and cols % 64 == 0 and cols % group == 0,
+          f"cols = {cols} must be a multiple of 64 and of the group ({group}: 32, 64 or 128)")
+    cs, ss = w4_shapes(rows, cols, group)
+    return _plane(codes, cs, torch.uint8, "codes"), _plane(scales, ss, _BF16, "scales")
+
+
+def ifq_w4_quantize(tensors, group, dev_status=None, stream=None):
+    """tensors: list of (R float32 [rows][cols], codes uint8, scales bf16), the last two written, of w4_shapes()."""
+    arr = (W4Tensor * len(tensors))()
+    for i, (R, codes, scales) in enumerate(tensors):
+        rows, cols = R.shape
+        c, s = _w4_buffers(codes, scales, rows, cols, group)
+        arr[i] = W4Tensor(_plane(R, (rows, cols), torch.float32, "R"), rows, cols, c, s)
+    dev = _device_of([t for ts in tensors for t in ts] + [dev_status])
+    _enqueue(dev, stream, load().ifq_w4_quantize, arr, len(tensors), group, _ptr(dev_status))
+
+
+def ifq_w4_dequantize(tensors, group, stream=None):
+    """tensors: list of (codes, scales, w bf16 [rows][cols]), w written."""
+    arr = (W4DqTensor * len(tensors))()
+    for i, (codes, scales, w) in enumerate(tensors):
+        rows, cols = w.shape
+        c, s = _w4_buffers(codes, scales, rows, cols, group)
+        arr[i] = W4DqTensor(c, s, rows, cols, _plane(w, (rows, cols), _BF16, "w"))
+    _enqueue(_device_of([t for ts in tensors for t in ts]), stream, load().ifq_w4_dequantize, arr, len(tensors), group)
+
+
+def ifq_w4_gemv(layers, group, B, dev_status=None, stream=None):
+    """layers: list of dicts with codes, scales, rows, cols, x_re, x_im (bf16 [B][cols/2]; x_im None: x_re is
+    [B][cols]) and y_re, y_im (float32 [B][rows/2]; y_im None: y_re is [B][rows])."""
+    arr = (W4Layer * len(layers))()
+    for i, d in enumerate(layers):
+        rows, cols = d["rows"], d["cols"]
+        c, s = _w4_buffers(d["codes"], d["scales"], rows, cols, group)
+        x_im, y_im = d.get("x_im"), d.get("y_im")
+        _need(y_im is None or rows % 2 == 0, "planar outputs need an even number of rows")
+        xs = (B, cols // (1 if x_im is None else 2))
+        ys = (B, rows // (1 if y_im is None else 2))
+        arr[i] = W4Layer(c, s, rows, cols, _plane(d["x_re"], xs, _BF16, "x_re"),
+                         None if x_im is None else _plane(x_im, xs, _BF16, "x_im"),
+                         _plane(d["y_re"], ys, torch.float32, "y_re"),
+                         None if y_im is None else _plane(y_im, ys, torch.float32, "y_im"))
+    dev = _device_of([d.get(n) for d in layers for n in ("codes", "scales", "x_re", "x_im", "y_re", "y_im")] +
+                     [dev_status])
+    _enqueue(dev, stream, load().ifq_w4_gemv, arr, len(layers), group, B, _ptr(dev_status))
+
+
+class Kv4Cache:
+    """A 4-bit key/value cache and the sequences of a step (ifq_kv4_cache), marshalled once: the tensors must
+    stay alive and in place; new lengths, pages and offsets are written into the same tensors.
+
+    records      uint8 [pages][kv_heads][page_tokens/16][32 dim + 256]
+    page_table   int32 [B][table_cols]
+    kv_lens      int32 [B], tokens of each sequence with its new ones
+    n_new        new tokens per sequence: the number of each, or the most that new_offsets gives
+    new_offsets  int32 [B+1] or None
+    rows         rows of the q, k, v and o buffers (default B n_new)"""
+
+    def __init__(self, records, page_table, kv_lens, dim, n_new=1, rows=None, new_offsets=None):
+        _need(records.dim() == 4 and records.shape[3] == 32 * dim + 256,
+              f"records must be [pages][kv_heads][page_tokens/16][{32 * dim + 256}]")
+        pages, kv_heads, tiles = records.shape[:3]
+        B = kv_lens.shape[0]
+        self.dim, self.kv_heads, self.B, self.n_new = dim, kv_heads, B, n_new
+        self.rows = B * n_new if rows is None else rows
+        self._keep = (records, page_table, kv_lens, new_offsets)
+        self.device = _device_of(self._keep)
+        _need(page_table.dim() == 2, "page_table must be [B][table_cols]")
+        self.desc = Kv4CacheDesc(
+            _plane(records, records.shape, torch.uint8, "records"), pages, 16 * tiles, kv_heads, dim, B, n_new, self.rows,
+            _plane(page_table, (B, page_table.shape[1]), torch.int32, "page_table"), page_table.shape[1],
+            _plane(kv_lens, (B,), torch.int32, "kv_lens"),
+            None if new_offsets is None else _plane(new_offsets, (B + 1,), torch.int32, "new_offsets"))
+
+    @staticmethod
+    def records_shape(pages, kv_heads, page_tokens, dim):
+        return pages, kv_heads, page_tokens // 16, 32 * dim + 256
+
+
+def _row_planes(cache, planes, width, dtype, what):
+    """Pointers and the common row stride of [rows][width] planes whose rows may be slices of wider ones."""
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    ld = planes[0].stride(0) if planes[0].shape[0] > 1 else max(width, planes[0].stride(0))
+    for t in planes:
+        _need(t.dtype in dtypes and t.dim() == 2 and t.shape[0] >= cache.rows and t.shape[1] == width and
+              t.stride(1) == 1 and (t.shape[0] == 1 or t.stride(0) == ld),
+              f"{what}: needs {dtypes[0]} [{cache.rows}][{width}] planes with one row stride")
+    _need(_device_of(planes) == cache.device, f"{what}: on another device than the cache")
+    return [t.data_ptr() for t in planes], ld
+
+
+def ifq_kv4_append(cache, k_re, k_im, v_re, v_im, dev_status=None, stream=None):
+    """Quantizes the new tokens' keys and values (float32 [rows][kv_heads dim], or column slices of wider
+    buffers with one row stride) into the cache."""
+    p, ld = _row_planes(cache, (k_re, k_im, v_re, v_im), cache.kv_heads * cache.dim, torch.float32, "k, v")
+    _enqueue(cache.device, stream, load().ifq_kv4_append, ctypes.byref(cache.desc), *p, ld, _ptr(dev_status))
+
+
+def ifq_kv4_read(cache, k_re, k_im, v_re, v_im, dev_status=None, stream=None):
+    """Writes the stored values of the new tokens (float32, laid out as for ifq_kv4_append)."""
+    p, ld = _row_planes(cache, (k_re, k_im, v_re, v_im), cache.kv_heads * cache.dim, torch.float32, "k, v")
+    _enqueue(cache.device, stream, load().ifq_kv4_read, ctypes.byref(cache.desc), *p, ld, _ptr(dev_status))
+
+
+def ifq_kv4_attention_workspace_bytes(cache, q_heads):
+    return int(load().ifq_kv4_attention_workspace_bytes(ctypes.byref(cache.desc), q_heads))
+
+
+def ifq_kv4_attention(cache, q_re, q_im, o_re, o_im, scale, workspace=None, dev_status=None, stream=None,
+                      workspace_bytes=None):
+    """q_re, q_im: float32 [rows][q_heads dim]; o_re, o_im: bf16, the same shape, written.  workspace: a device
+    buffer of ifq_kv4_attention_workspace_bytes(cache, q_heads) bytes (no initial contents needed)."""
+    width = q_re.shape[1]
+    _need(width % cache.dim == 0, "q's row must be a whole number of heads")
+    q, ldq = _row_planes(cache, (q_re, q_im), width, torch.float32, "q")
+    o, ldo = _row_planes(cache, (o_re, o_im), width, _BF16, "o")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace_bytes is not None:
+        nbytes = workspace_bytes
+    _enqueue(cache.device, stream, load().ifq_kv4_attention, ctypes.byref(cache.desc), width // cache.dim, *q, ldq,
+             float(scale), *o, ldo, _ptr(workspace), nbytes, _ptr(dev_status))
 
 
 # Raw entry point for callers that build ctypes descriptors themselves.

@@ -343,4 +343,150 @@ ifq_status ifq_gemm(const ifq_layer* layers, int count, int T, int64_t M, uint32
   return ifq_gemm_wait_limit(layers, count, T, M, IFQ_WAIT_LIMIT_NS, dev_status, stream);
 }
 
+// ------------------------------------------------------------------ 4-bit layers and cache
+namespace {
+
+bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
+
+// Shapes of one 4-bit tensor; `units` adds up the call's tiles (the launches' grids are 32-bit).
+ifq_status check_w4_shape(int64_t rows, int64_t cols, int group, int64_t* units) {
+  if (rows < 1 || cols < 64 || cols % 64 || cols % group) return IFQ_ERR_SHAPE;
+  if (rows > (int64_t)1 << 30 || cols > (int64_t)1 << 30 || rows > ((int64_t)1 << 40) / cols) return IFQ_ERR_SHAPE;
+  *units += ifq::w4_units(rows, cols, group);
+  return *units <= (int64_t)1 << 31 ? IFQ_OK : IFQ_ERR_SHAPE;
+}
+
+ifq_status check_w4_call(const void* items, int count, int group) {
+  if (!items) return IFQ_ERR_NULL;
+  if (count < 1 || count > IFQ_MAX_GROUP) return IFQ_ERR_COUNT;
+  return w4_group_ok(group) ? IFQ_OK : IFQ_ERR_SHAPE;
+}
+
+ifq_status check_kv4(const ifq_kv4_cache* c) {
+  if (!c || !c->records || !c->page_table || !c->kv_lens) return IFQ_ERR_NULL;
+  if (c->pages < 1 || c->pages > 0x7FFFFFFF || c->page_tokens < 16 || c->page_tokens > 65536 || c->page_tokens % 16)
+    return IFQ_ERR_SHAPE;
+  if (c->kv_heads < 1 || c->kv_heads > 1024 || (c->dim != 32 && c->dim != 64 && c->dim != 128)) return IFQ_ERR_SHAPE;
+  if (c->B < 1 || c->B > 65535 || c->table_cols < 1 || c->table_cols > (int64_t)1 << 26) return IFQ_ERR_SHAPE;
+  // positions are 32-bit
+  if (c->table_cols * c->page_tokens > ((int64_t)1 << 31) - 65536) return IFQ_ERR_SHAPE;
+  if (c->rows < 1 || c->rows > 0x7FFFFFFF) return IFQ_ERR_SHAPE;
+  if (c->n_new < 1) return IFQ_ERR_BATCH;
+  if (!c->new_offsets && (int64_t)c->B * c->n_new > c->rows) return IFQ_ERR_SHAPE;
+  if (!aligned16(c->records) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->kv_lens) & 3u) || (reinterpret_cast<uintptr_t>(c->new_offsets) & 3u))
+    return IFQ_ERR_ALIGN;
+  return IFQ_OK;
+}
+
+ifq_status check_kv4_rows(const ifq_kv4_cache* c, const void* a, const void* b, const void* d, const void* e,
+                          int64_t ld) {
+  ifq_status st = check_kv4(c);
+  if (st != IFQ_OK) return st;
+  if (!a || !b || !d || !e) return IFQ_ERR_NULL;
+  if (ld < (int64_t)c->kv_heads * c->dim || ld % 4 || ld > (int64_t)1 << 30) return IFQ_ERR_SHAPE;
+  if ((int64_t)c->n_new * c->kv_heads * c->dim > (int64_t)1 << 38) return IFQ_ERR_SHAPE;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned16(e)) return IFQ_ERR_ALIGN;
+  return check_device();
+}
+
+ifq_status check_kv4_attention(const ifq_kv4_cache* c, int q_heads) {
+  ifq_status st = check_kv4(c);
+  if (st != IFQ_OK) return st;
+  if (c->n_new > IFQ_KV4_MAX_NEW) return IFQ_ERR_BATCH;
+  if (q_heads < c->kv_heads || q_heads % c->kv_heads || q_heads > 4096) return IFQ_ERR_SHAPE;
+  // (key/value head, query tile) is one grid dimension
+  if ((int64_t)c->kv_heads * ((int64_t)c->n_new * (q_heads / c->kv_heads) / 4 + 1) > 65535) return IFQ_ERR_SHAPE;
+  return IFQ_OK;
+}
+
+}  // namespace
+
+ifq_status ifq_w4_quantize(const ifq_w4_tensor* tensors, int count, int group, uint32_t* dev_status,
+                           ifq_stream_t stream) {
+  ifq_status st = check_w4_call(tensors, count, group);
+  if (st != IFQ_OK) return st;
+  int64_t units = 0;
+  for (int i = 0; i < count; ++i) {
+    const ifq_w4_tensor& t = tensors[i];
+    if (!t.R || !t.codes || !t.scales) return IFQ_ERR_NULL;
+    if ((st = check_w4_shape(t.rows, t.cols, group, &units)) != IFQ_OK) return st;
+    if (!aligned16(t.R) || !aligned16(t.codes) || !aligned16(t.scales)) return IFQ_ERR_ALIGN;
+  }
+  if ((st = check_device()) != IFQ_OK) return st;
+  return from_cuda(ifq::launch_w4_quantize(tensors, count, group, dev_status, as_stream(stream)));
+}
+
+ifq_status ifq_w4_dequantize(const ifq_w4_dqtensor* tensors, int count, int group, ifq_stream_t stream) {
+  ifq_status st = check_w4_call(tensors, count, group);
+  if (st != IFQ_OK) return st;
+  int64_t units = 0;
+  for (int i = 0; i < count; ++i) {
+    const ifq_w4_dqtensor& t = tensors[i];
+    if (!t.codes || !t.scales || !t.w) return IFQ_ERR_NULL;
+    if ((st = check_w4_shape(t.rows, t.cols, group, &units)) != IFQ_OK) return st;
+    if (!aligned16(t.codes) || !aligned16(t.scales) || !aligned16(t.w)) return IFQ_ERR_ALIGN;
+  }
+  if ((st = check_device()) != IFQ_OK) return st;
+  return from_cuda(ifq::launch_w4_dequantize(tensors, count, group, as_stream(stream)));
+}
+
+ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, uint32_t* dev_status,
+                       ifq_stream_t stream) {
+  ifq_status st = check_w4_call(layers, count, group);
+  if (st != IFQ_OK) return st;
+  int64_t units = 0;
+  for (int i = 0; i < count; ++i) {
+    const ifq_w4_layer& l = layers[i];
+    if (!l.codes || !l.scales || !l.x_re || !l.y_re) return IFQ_ERR_NULL;
+    if ((st = check_w4_shape(l.rows, l.cols, group, &units)) != IFQ_OK) return st;
+    if (l.y_im && (l.rows & 1)) return IFQ_ERR_SHAPE;
+    if (!aligned16(l.codes) || !aligned16(l.scales) || !aligned16(l.x_re) || !aligned16(l.x_im) ||
+        !aligned16(l.y_re) || !aligned16(l.y_im))
+      return IFQ_ERR_ALIGN;
+  }
+  if (B < 1 || B > IFQ_MAX_GEMV_BATCH) return IFQ_ERR_BATCH;
+  if ((st = check_device()) != IFQ_OK) return st;
+  return from_cuda(ifq::launch_w4_gemv(layers, count, group, B, dev_status, as_stream(stream)));
+}
+
+ifq_status ifq_kv4_append(const ifq_kv4_cache* cache, const float* k_re, const float* k_im, const float* v_re,
+                          const float* v_im, int64_t ld, uint32_t* dev_status, ifq_stream_t stream) {
+  ifq_status st = check_kv4_rows(cache, k_re, k_im, v_re, v_im, ld);
+  if (st != IFQ_OK) return st;
+  return from_cuda(ifq::launch_kv4_append(*cache, k_re, k_im, v_re, v_im, ld, dev_status, as_stream(stream)));
+}
+
+ifq_status ifq_kv4_read(const ifq_kv4_cache* cache, float* k_re, float* k_im, float* v_re, float* v_im, int64_t ld,
+                        uint32_t* dev_status, ifq_stream_t stream) {
+  ifq_status st = check_kv4_rows(cache, k_re, k_im, v_re, v_im, ld);
+  if (st != IFQ_OK) return st;
+  return from_cuda(ifq::launch_kv4_read(*cache, k_re, k_im, v_re, v_im, ld, dev_status, as_stream(stream)));
+}
+
+size_t ifq_kv4_attention_workspace_bytes(const ifq_kv4_cache* cache, int q_heads) {
+  if (check_kv4_attention(cache, q_heads) != IFQ_OK) return 0;
+  return ifq::kv4_attention_workspace_bytes(*cache, q_heads / cache->kv_heads);
+}
+
+ifq_status ifq_kv4_attention(const ifq_kv4_cache* cache, int q_heads, const float* q_re, const float* q_im,
+                             int64_t ldq, float scale, uint16_t* o_re, uint16_t* o_im, int64_t ldo, void* workspace,
+                             size_t workspace_bytes, uint32_t* dev_status, ifq_stream_t stream) {
+  ifq_status st = check_kv4_attention(cache, q_heads);
+  if (st != IFQ_OK) return st;
+  if (!q_re || !q_im || !o_re || !o_im) return IFQ_ERR_NULL;
+  const int64_t width = (int64_t)q_heads * cache->dim;
+  if (ldq < width || ldq % 4 || ldq > (int64_t)1 << 30 || ldo < width || ldo % 2 || ldo > (int64_t)1 << 30)
+    return IFQ_ERR_SHAPE;
+  if (!aligned16(q_re) || !aligned16(q_im) || ((reinterpret_cast<uintptr_t>(o_re) | reinterpret_cast<uintptr_t>(o_im)) & 3u))
+    return IFQ_ERR_ALIGN;
+  const int shared = q_heads / cache->kv_heads;
+  const size_t need = ifq::kv4_attention_workspace_bytes(*cache, shared);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return IFQ_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return IFQ_ERR_ALIGN;
+  if ((st = check_device()) != IFQ_OK) return st;
+  return from_cuda(ifq::launch_kv4_attention(*cache, shared, q_re, q_im, ldq, scale, o_re, o_im, ldo, workspace,
+                                             dev_status, as_stream(stream)));
+}
+
 }  // extern "C"

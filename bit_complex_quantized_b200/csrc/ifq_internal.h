@@ -64,6 +64,22 @@ inline bool any_narrow_k(const ifq_layer* L, int count) {
 bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw);
 
+// 4-bit layers with group scales (w4_quantize.cu, w4_gemv.cu).
+int64_t w4_units(int64_t rows, int64_t cols, int group);
+cudaError_t launch_w4_quantize(const ifq_w4_tensor* t, int count, int group, uint32_t* dev_status, cudaStream_t s);
+cudaError_t launch_w4_dequantize(const ifq_w4_dqtensor* t, int count, int group, cudaStream_t s);
+cudaError_t launch_w4_gemv(const ifq_w4_layer* L, int count, int group, int B, uint32_t* dev_status, cudaStream_t s);
+
+// 4-bit key/value cache (kv4_cache.cu, kv4_attention.cu); shared = query heads of a key/value head.
+cudaError_t launch_kv4_append(const ifq_kv4_cache& c, const float* k_re, const float* k_im, const float* v_re,
+                              const float* v_im, int64_t ld, uint32_t* dev_status, cudaStream_t s);
+cudaError_t launch_kv4_read(const ifq_kv4_cache& c, float* k_re, float* k_im, float* v_re, float* v_im, int64_t ld,
+                            uint32_t* dev_status, cudaStream_t s);
+size_t kv4_attention_workspace_bytes(const ifq_kv4_cache& c, int shared);
+cudaError_t launch_kv4_attention(const ifq_kv4_cache& c, int shared, const float* q_re, const float* q_im, int64_t ldq,
+                                 float scale, uint16_t* o_re, uint16_t* o_im, int64_t ldo, void* ws,
+                                 uint32_t* dev_status, cudaStream_t s);
+
 cudaError_t launch_gemm(const ifq_layer* L, int count, int T, int64_t M, uint64_t wait_ns, uint32_t* dev_status,
                         cudaStream_t s);
 

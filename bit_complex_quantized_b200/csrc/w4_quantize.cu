@@ -1,0 +1,211 @@
+// Layers with 4-bit weights and group scales: the quantizer and the values the codes stand for.
+//
+// For every group of G consecutive columns of a row of R: s = bf16(max |w| * c), c the float32 nearest
+// to 1/7 (product in float32, both roundings to nearest-even), q = rint(w / s) half-even of the exact quotient, clamped
+// to [-7, 7], 0 where s = 0; stored as q + 8.  Codes are chosen against the rounded scale, so the
+// scale's rounding adds nothing to |w - s q| <= s / 2 but the clamp of a largest entry whose scale
+// was rounded down (at most s 7 2^-9 more).
+//
+// HBM-bound: 4 bytes read and 0.5 + 2 / G written per weight.  A warp takes 16 rows x max(64, G) columns,
+// so that every group's maximum stays inside four lanes, loads are 32-byte runs per lane that fill
+// whole 128-byte lines across a quad of lanes, and the codes leave as one 512-byte store per tile.
+#include "ifq_internal.h"
+#include "q4_common.cuh"
+
+namespace ifq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct QArg {
+  const float* R;
+  uint8_t* codes;
+  uint16_t* scales;
+  uint16_t* out;  // dequantized bf16 [rows][cols]
+  int64_t rows, cols;
+  int64_t unit_begin;  // first unit (16 rows x U columns) of the tensor in the call
+};
+
+struct QParams {
+  QArg t[IFQ_MAX_GROUP];
+  int count;
+  int64_t units;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ int find_tensor(const QParams& p, int64_t unit) {
+  int i = 0;
+  while (i + 1 < p.count && unit >= p.t[i + 1].unit_begin) ++i;
+  return i;
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constant__ QParams p) {
+  constexpr int U = G > 64 ? G : 64, C = U / 32;      // columns and 32-column chunks of a unit
+  constexpr int kPer = G / 32;                        // chunks of a group
+  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (unit >= p.units) return;
+  const QArg& T = p.t[find_tensor(p, unit)];
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t cu = T.cols / U, local = unit - T.unit_begin;
+  const int64_t rt = local / cu, c0 = (local % cu) * U;
+
+  float v[2][C][8];
+  bool bad = false;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = rt * 16 + g + 8 * h;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      if (r < T.rows) {
+        const float4* src = reinterpret_cast<const float4*>(T.R + r * T.cols + c0 + 32 * c + 8 * t);
+        a = __ldcs(src);
+        b = __ldcs(src + 1);
+      }
+      v[h][c][0] = a.x; v[h][c][1] = a.y; v[h][c][2] = a.z; v[h][c][3] = a.w;
+      v[h][c][4] = b.x; v[h][c][5] = b.y; v[h][c][6] = b.z; v[h][c][7] = b.w;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(fabsf(v[h][c][j]) <= 3.402823466e38f)) {
+          v[h][c][j] = 0.0f;
+          bad = true;
+        }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, IFQ_DEV_NONFINITE);
+
+  uint32_t words[2][C];
+#pragma unroll
+  for (int c0g = 0; c0g < C; c0g += kPer) {
+    uint32_t sbits[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float m = 0.0f;
+#pragma unroll
+      for (int c = c0g; c < c0g + kPer; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[h][c][j]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(m, 1.0f / 7.0f));
+      sbits[h] = __bfloat16_as_ushort(sb);
+      const float s = __bfloat162float(sb);
+      const float inv = s >= 1e-30f ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+      for (int c = c0g; c < c0g + kPer; ++c) {
+        uint32_t n[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float q = 0.0f;
+          if (s > 0.0f) q = fminf(fmaxf(q4_round_quotient(v[h][c][j], s, inv), -7.0f), 7.0f);
+          n[j] = (uint32_t)((int)q + 8);
+        }
+        words[h][c] = q4_pack_word(n);
+      }
+    }
+    if (t == 0)
+      reinterpret_cast<uint32_t*>(T.scales)[(rt * (T.cols / G) + (c0 + 32 * c0g) / G) * 8 + g] =
+          sbits[0] | (sbits[1] << 16);
+  }
+#pragma unroll
+  for (int k = 0; k < C / 2; ++k) {
+    uint4 w = make_uint4(words[0][2 * k], words[1][2 * k], words[0][2 * k + 1], words[1][2 * k + 1]);
+    reinterpret_cast<uint4*>(T.codes)[(rt * (T.cols / 64) + c0 / 64 + k) * 32 + lane] = w;
+  }
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads) w4_dequant_kernel(const __grid_constant__ QParams p) {
+  constexpr int U = G > 64 ? G : 64;
+  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (unit >= p.units) return;
+  const QArg& T = p.t[find_tensor(p, unit)];
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t cu = T.cols / U, local = unit - T.unit_begin;
+  const int64_t rt = local / cu, c0 = (local % cu) * U;
+  uint4 w[U / 64];
+#pragma unroll
+  for (int k = 0; k < U / 64; ++k)
+    w[k] = ldg_stream(reinterpret_cast<const uint4*>(T.codes) + (rt * (T.cols / 64) + c0 / 64 + k) * 32 + lane);
+#pragma unroll
+  for (int k = 0; k < U / 64; ++k)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t sc = __ldg(reinterpret_cast<const uint32_t*>(T.scales) +
+                                (rt * (T.cols / G) + (c0 + 64 * k + 32 * c) / G) * 8 + g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t r = rt * 16 + g + 8 * h;
+        const float s = h ? bf16_hi(sc) : bf16_lo(sc);
+        const uint32_t word = c ? (h ? w[k].w : w[k].z) : (h ? w[k].y : w[k].x);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = (float)((int)((word >> (4 * i)) & 15u) - 8);
+          const float hi = (float)((int)((word >> (4 * i + 16)) & 15u) - 8);
+          o[i] = pack_bf16(s * lo, s * hi);
+        }
+        if (r < T.rows)
+          __stcs(reinterpret_cast<uint4*>(T.out + r * T.cols + c0 + 64 * k + 32 * c + 8 * t),
+                 make_uint4(o[0], o[1], o[2], o[3]));
+      }
+    }
+}
+
+template <typename Fill>
+void fill(QParams& p, int count, int group, Fill f) {
+  p.count = count;
+  const int64_t U = group > 64 ? group : 64;
+  int64_t units = 0;
+  for (int i = 0; i < count; ++i) {
+    f(p.t[i], i);
+    p.t[i].unit_begin = units;
+    units += (p.t[i].rows + 15) / 16 * (p.t[i].cols / U);
+  }
+  p.units = units;
+}
+
+}  // namespace
+
+int64_t w4_units(int64_t rows, int64_t cols, int group) { return (rows + 15) / 16 * (cols / (group > 64 ? group : 64)); }
+
+cudaError_t launch_w4_quantize(const ifq_w4_tensor* ts, int count, int group, uint32_t* dev_status, cudaStream_t s) {
+  QParams p = {};
+  fill(p, count, group, [&](QArg& a, int i) {
+    a.R = ts[i].R;
+    a.codes = ts[i].codes;
+    a.scales = ts[i].scales;
+    a.rows = ts[i].rows;
+    a.cols = ts[i].cols;
+  });
+  p.status = dev_status;
+  const unsigned grid = (unsigned)((p.units + kWarps - 1) / kWarps);
+  if (group == 32) w4_quant_kernel<32><<<grid, kThreads, 0, s>>>(p);
+  else if (group == 64) w4_quant_kernel<64><<<grid, kThreads, 0, s>>>(p);
+  else w4_quant_kernel<128><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_w4_dequantize(const ifq_w4_dqtensor* ts, int count, int group, cudaStream_t s) {
+  QParams p = {};
+  fill(p, count, group, [&](QArg& a, int i) {
+    a.codes = const_cast<uint8_t*>(ts[i].codes);
+    a.scales = const_cast<uint16_t*>(ts[i].scales);
+    a.out = ts[i].w;
+    a.rows = ts[i].rows;
+    a.cols = ts[i].cols;
+  });
+  const unsigned grid = (unsigned)((p.units + kWarps - 1) / kWarps);
+  if (group == 32) w4_dequant_kernel<32><<<grid, kThreads, 0, s>>>(p);
+  else if (group == 64) w4_dequant_kernel<64><<<grid, kThreads, 0, s>>>(p);
+  else w4_dequant_kernel<128><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ifq

@@ -51,7 +51,7 @@ typedef enum {
   IFQ_ERR_SHAPE = 2,       /* a size is zero, negative, odd where it must be even, or not a multiple the call needs */
   IFQ_ERR_ALIGN = 3,       /* a pointer is not 16-byte aligned */
   IFQ_ERR_STAGES = 4,      /* T outside 1..IFQ_MAX_STAGES */
-  IFQ_ERR_BATCH = 5,       /* B outside 1..IFQ_MAX_GEMV_BATCH, or M < 1 */
+  IFQ_ERR_BATCH = 5,       /* B outside 1..IFQ_MAX_GEMV_BATCH, or M < 1; new tokens of a cache call outside their range */
   IFQ_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than ifq_quantize_workspace_bytes() */
   IFQ_ERR_CUDA = 7,        /* a CUDA runtime call failed (launch error, no device, ...) */
   IFQ_ERR_UNSUPPORTED = 8, /* the device is not sm_100 */
@@ -66,6 +66,8 @@ typedef enum {
 /* Device status bits, OR-ed into *dev_status by kernels. */
 #define IFQ_DEV_NONFINITE 0x1u /* a weight was NaN or Inf; it was quantized as 0 (code 0) */
 #define IFQ_DEV_TIMEOUT 0x2u   /* a bounded pipeline wait gave up; outputs of that call are invalid */
+#define IFQ_DEV_RANGE 0x4u     /* a length, row offset or page number in device memory was outside its range
+                                  (the 4-bit cache); what it named was skipped */
 
 const char* ifq_status_string(ifq_status s);
 
@@ -321,7 +323,8 @@ ifq_status ifq_dequantize(const ifq_dqtensor* tensors, int count, int T, ifq_str
  * The attention score of the complex model, Re(q^T conj(k)) ("Fairy2i write-up"
  * §2.2; "iFairy talk notes" §2.1.4), equals the real dot product of the stacked
  * vectors [q_re, q_im] and [k_re, k_im], so the planar outputs feed a standard
- * real attention kernel directly; the library has no score kernel of its own.
+ * real attention kernel directly, or the 4-bit cache and its decode attention
+ * (ifq_kv4_append, ifq_kv4_attention below).
  * ------------------------------------------------------------------------- */
 typedef struct {
   const uint8_t* codes_u;
@@ -404,6 +407,181 @@ ifq_status ifq_gemm(const ifq_layer* layers, int count, int T, int64_t M, uint32
  * IFQ_ERR_SHAPE. */
 ifq_status ifq_gemm_wait_limit(const ifq_layer* layers, int count, int T, int64_t M, uint64_t wait_limit_ns,
                                uint32_t* dev_status, ifq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Layers with 4-bit weights and group scales
+ *
+ * A real layer R (rows outputs x cols inputs, the R of
+ * ifq_widely_linear_from_real) kept at 4 bits instead of 2-bit complex codes,
+ * for the layers of a model that need more bits (a logits head over the
+ * concatenated planes, first and last layers).  It acts on the same planar x and
+ * writes the same planar y as the converted layer with N = rows/2, K = cols/2.
+ *
+ * Per group of `group` consecutive columns of a row:
+ *   s = max |w| times the float32 nearest to 1/7, the product rounded to float32 and
+ *       then to bf16 (nearest-even);
+ *   q = w / s rounded half-even (of the exact quotient), clamped to [-7, 7]; 0 where s = 0;
+ *   w_hat = s q.
+ *
+ * Layout.  Tiles of 16 rows x 64 columns, 512 bytes each, in the operand order
+ * of the tensor cores: codes uint8 [ceil(rows/16)][cols/64][512].  Entry (row r,
+ * column k) is held as q + 8 in 4 bits of the little-endian 32-bit word
+ *   2 ((k % 64) / 32) + (r % 16) / 8   of the 16 bytes   4 (r % 8) + (k % 32) / 8
+ * of tile (r / 16, k / 64), from bit 4 ((k % 8) / 2) + 16 (k % 2).  Rows past
+ * `rows` in the last tile hold code 8 (zero).  Scales are bf16 bit patterns
+ * [ceil(rows/16)][cols/group][16], row r at index 2 (r % 8) + (r % 16) / 8.
+ *
+ *   rows    1..2^30     cols   a multiple of 64 and of group, <= 2^30
+ *   group   32, 64 or 128, the same for every tensor or layer of a call
+ *   count   1..IFQ_MAX_GROUP tensors or layers
+ * Pointers must be 16-byte aligned; another group is IFQ_ERR_SHAPE.
+ *
+ * ifq_w4_quantize     R [rows][cols] float32 -> codes, scales.  A NaN or Inf
+ *                     weight is quantized as 0 and sets IFQ_DEV_NONFINITE.
+ * ifq_w4_dequantize   codes, scales -> w [rows][cols], s q rounded to bf16
+ *                     (nearest-even), for the forward pass of
+ *                     quantization-aware training and for prefill by a dense
+ *                     matrix product.
+ * ifq_w4_gemv         y = R_hat [x_re; x_im] for B = 1..IFQ_MAX_GEMV_BATCH
+ *                     tokens, all layers in one launch.
+ *   x_re, x_im   [B][cols/2] bf16 bit patterns; or x_im NULL and x_re [B][cols]
+ *   y_re, y_im   [B][rows/2] float32, overwritten (rows even); or y_im NULL and
+ *                y_re [B][rows]
+ * Products of codes and activations are exact and accumulate in float32 within a
+ * group, the scales multiply group sums in float32, and the order of all sums is
+ * fixed by the shapes and the call's layers, so results are bit-reproducible.  An output that is not
+ * finite (a NaN or Inf activation, or an overflow) sets IFQ_DEV_NONFINITE.
+ * dev_status may be NULL.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  const float* R;
+  int64_t rows;
+  int64_t cols;
+  uint8_t* codes;
+  uint16_t* scales;
+} ifq_w4_tensor;
+
+ifq_status ifq_w4_quantize(const ifq_w4_tensor* tensors, int count, int group, uint32_t* dev_status,
+                           ifq_stream_t stream);
+
+typedef struct {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  int64_t rows;
+  int64_t cols;
+  uint16_t* w;
+} ifq_w4_dqtensor;
+
+ifq_status ifq_w4_dequantize(const ifq_w4_dqtensor* tensors, int count, int group, ifq_stream_t stream);
+
+typedef struct {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  int64_t rows;
+  int64_t cols;
+  const uint16_t* x_re;
+  const uint16_t* x_im;
+  float* y_re;
+  float* y_im;
+} ifq_w4_layer;
+
+ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, uint32_t* dev_status,
+                       ifq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Key/value cache in 4 bits, and the decode attention over it
+ * ("Fairy2i write-up" §2.2 items 2-3; "iFairy talk notes" §2.1.4)
+ *
+ * Takes the rotated k and the v that the products write (float32, planar) and
+ * answers q with Re(q^T conj(k)) attention, the planes of v summed separately, as
+ * the bf16 planes the next product reads: no kernel lies between the calls.
+ *
+ * A head has `dim` complex entries (32, 64 or 128), D = 2 dim stacked ones.  Each
+ * plane of a token's k or v of a head is a group:
+ *   m = min x as bf16;  s = c max x - c min x as bf16, c the float32 nearest to
+ *   1/15 (each step rounded to float32);
+ *   n = (x - m) / s rounded half-even (of the exact quotient), clamped to
+ *   [0, 15], 0 where s = 0;  the stored value is s n + m.
+ * NaN and Inf entries are stored as 0 and set IFQ_DEV_NONFINITE; larger
+ * magnitudes than bf16 holds are stored as the largest bf16.
+ *
+ * records       uint8 [pages][kv_heads][page_tokens/16][32 dim + 256], one record per 16
+ *               tokens of a head: keys (8 D bytes, a 16 x D tile of the layout
+ *               above, row = token % 16), values (8 D bytes), key parameters and
+ *               value parameters (128 bytes each: per token bf16 s_re, m_re, s_im,
+ *               m_im).  Value entry (token r of 16, stacked entry d): word
+ *               2 ((d % 64) / 32) + r / 8 of the 16 bytes 4 ((d % 32) / 4) + (r % 8) / 2
+ *               of the 512 bytes d / 64, from bit 4 (d % 4) + 16 (r % 2).
+ *               16 (D + 16) bytes per 16 tokens: 3.5 times less than bf16 at dim 64.
+ * page_table    int32 [B][table_cols]: the page that holds positions
+ *               j page_tokens .. of each sequence; entries behind kv_lens unused
+ * kv_lens       int32 [B]: tokens of each sequence WITH the call's new ones
+ * new tokens    a sequence's new tokens are its last ones, and consecutive rows
+ *               of q, k, v and o: rows new_offsets[b] .. new_offsets[b+1] - 1
+ *               (int32 [B+1], at most n_new each), or with new_offsets NULL
+ *               n_new rows each.  rows: allocated rows of those buffers; rows that
+ *               belong to no sequence are neither read nor written.
+ *   pages 1..2^31-1     page_tokens  a multiple of 16, 16..65536
+ *   kv_heads 1..1024    B 1..65535    n_new >= 1    table_cols 1..2^26
+ * page_table, kv_lens and new_offsets are device memory, read when the call's
+ * work runs (so a captured graph serves growing lengths).  What they name is checked
+ * there: a sequence whose offsets decrease, leave 0..rows or give more
+ * than n_new rows is skipped; one whose length is less than its new
+ * tokens or more than table_cols * page_tokens counts as empty; a page number
+ * outside 0..pages-1 is not touched (appending skips the token, attention
+ * leaves its keys out, reading gives 0).  Each sets IFQ_DEV_RANGE.
+ * Two sequences may share pages that neither appends to; pages that a call
+ * appends to must not be shared.
+ *
+ * ifq_kv4_append     k_re, k_im, v_re, v_im [rows][kv_heads dim] float32, rows ld
+ *                    elements apart: quantized into the records.  Any n_new.
+ * ifq_kv4_read       the stored values of the same tokens, as float32 (s n + m
+ *                    rounded once): what attention uses.
+ * ifq_kv4_attention  q_re, q_im [rows][q_heads dim] float32, rows ldq apart, head h
+ *                    reading key/value head h / (q_heads / kv_heads); new token i of a
+ *                    sequence sees positions 0 .. len - n + i (itself included,
+ *                    so append first).  o_re, o_im [rows][q_heads dim] bf16, rows
+ *                    ldo apart.  score = scale Re(q^T conj(k)).  n_new <=
+ *                    IFQ_KV4_MAX_NEW.  A row that sees no key is 0.  q enters as two bf16
+ *                    terms (2^-16 relative), the weights of v likewise; sums and the
+ *                    softmax's maximum and sum are float32; partial results are
+ *                    joined in a fixed order (bit-reproducible).  A NaN or Inf in q
+ *                    sets IFQ_DEV_NONFINITE and makes that row NaN.
+ *   workspace        device scratch of ifq_kv4_attention_workspace_bytes() bytes,
+ *                    16-byte aligned, no initial contents needed; calls that share it
+ *                    must not overlap on the GPU.  May be NULL when that is 0.
+ * Strides are multiples of 4 elements (o: 2) and at least the row's width, else
+ * IFQ_ERR_SHAPE; q, k, v pointers and records are 16-byte aligned, o 4-byte.
+ * n_new outside its range is IFQ_ERR_BATCH.  dev_status may be NULL.
+ * ------------------------------------------------------------------------- */
+#define IFQ_KV4_MAX_NEW 16
+
+typedef struct {
+  uint8_t* records;
+  int64_t pages;
+  int32_t page_tokens;
+  int32_t kv_heads;
+  int32_t dim;
+  int32_t B;
+  int32_t n_new;
+  int64_t rows;
+  const int32_t* page_table;
+  int64_t table_cols;
+  const int32_t* kv_lens;
+  const int32_t* new_offsets;
+} ifq_kv4_cache;
+
+ifq_status ifq_kv4_append(const ifq_kv4_cache* cache, const float* k_re, const float* k_im, const float* v_re,
+                          const float* v_im, int64_t ld, uint32_t* dev_status, ifq_stream_t stream);
+
+ifq_status ifq_kv4_read(const ifq_kv4_cache* cache, float* k_re, float* k_im, float* v_re, float* v_im, int64_t ld,
+                        uint32_t* dev_status, ifq_stream_t stream);
+
+size_t ifq_kv4_attention_workspace_bytes(const ifq_kv4_cache* cache, int q_heads);
+
+ifq_status ifq_kv4_attention(const ifq_kv4_cache* cache, int q_heads, const float* q_re, const float* q_im,
+                             int64_t ldq, float scale, uint16_t* o_re, uint16_t* o_im, int64_t ldo, void* workspace,
+                             size_t workspace_bytes, uint32_t* dev_status, ifq_stream_t stream);
 
 #ifdef __cplusplus
 }
