@@ -20,6 +20,7 @@ from ._lib import (  # noqa: F401
     Kv4Cache,
     LayerSet,
     LIB_PATH,
+    W4LayerSet,
     ifq_dequantize,
     ifq_gemm,
     ifq_gemm_wait_limit,

@@ -161,11 +161,11 @@ def load():
     lib.ifq_gemm_wait_limit.restype = i32
     lib.ifq_gemm_wait_limit.argtypes = [ctypes.POINTER(Layer), i32, i32, i64, ctypes.c_uint64, vp, vp]
     lib.ifq_w4_quantize.restype = i32
-    lib.ifq_w4_quantize.argtypes = [ctypes.POINTER(W4Tensor), i32, i32, vp, vp]
+    lib.ifq_w4_quantize.argtypes = [vp, i32, i32, vp, vp]
     lib.ifq_w4_dequantize.restype = i32
-    lib.ifq_w4_dequantize.argtypes = [ctypes.POINTER(W4DqTensor), i32, i32, vp]
+    lib.ifq_w4_dequantize.argtypes = [vp, i32, i32, vp]
     lib.ifq_w4_gemv.restype = i32
-    lib.ifq_w4_gemv.argtypes = [ctypes.POINTER(W4Layer), i32, i32, i32, vp, vp]
+    lib.ifq_w4_gemv.argtypes = [vp, i32, i32, i32, vp, vp]
     kvp = ctypes.POINTER(Kv4CacheDesc)
     lib.ifq_kv4_append.restype = i32
     lib.ifq_kv4_append.argtypes = [kvp, vp, vp, vp, vp, i64, vp, vp]
@@ -364,85 +364,122 @@ def ifq_gemm_wait_limit(layers, T, M, wait_limit_ns, dev_status=None, stream=Non
 
 
 # ------------------------------------------------------------------ 4-bit layers and cache
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+# A decode step makes these calls every few microseconds of GPU time, so the checks build no message and no
+# object unless they fail, and descriptors are flat arrays of 64-bit words.
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values or their bit patterns
+_F32 = (torch.float32,)
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _device_of(tensors):
-    """The one CUDA device of all given tensors (None entries are skipped)."""
-    devs = {t.device for t in tensors if t is not None}
-    _need(len(devs) == 1 and next(iter(devs)).type == "cuda", "all tensors of a call must be on one CUDA device")
-    return next(iter(devs))
+def _enqueue(index, stream, fn, *args):
+    """fn(*args, stream) with CUDA device `index` current; stream: that device's current one by default."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _enqueue(index, stream, fn, *args)
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _current_raw_stream is not None:
+        raw = _current_raw_stream(index)
+    else:
+        raw = torch.cuda.current_stream().cuda_stream
+    status = fn(*args, raw)
+    if status != 0:
+        _check(status)
 
 
-def _enqueue(device, stream, fn, *args):
-    """fn(*args, stream) with the tensors' device current; stream: that device's current one by default."""
-    with torch.cuda.device(device):
-        _check(fn(*args, _stream(stream)))
-
-
-def _plane(t, shape, dtype, what):
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    _need(t.dtype in dtypes and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{what}: needs a contiguous {dtypes[0]} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+def _plane(t, shape, dtypes, index, what):
+    """Address of a contiguous tensor of the given shape and type on CUDA device `index` (None: any one)."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{what}: needs a contiguous {dtypes[0]} tensor of shape {shape}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{what}: all tensors of a call must be on one CUDA device, got {t.device}")
     return t.data_ptr()
 
 
-_BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values or their bit patterns
+def _status_ptr(t, index):
+    """Address of an optional device status word."""
+    if t is None:
+        return None
+    if t.get_device() != index or t.element_size() != 4 or t.numel() < 1:
+        raise ValueError("dev_status must be a 32-bit integer tensor on the call's device")
+    return t.data_ptr()
 
 
 def w4_shapes(rows, cols, group):
     """Shapes of the codes (uint8) and scales (bf16) of a 4-bit [rows][cols] layer."""
-    return ((rows + 15) // 16, cols // 64, 512), ((rows + 15) // 16, cols // group, 16)
+    tiles = (rows + 15) // 16
+    return (tiles, cols // 64, 512), (tiles, cols // group, 16)
 
 
-def _w4_buffers(codes, scales, rows, cols, group):
-    _need(group in (32, 64, 128) and cols > 0 and cols % 64 == 0 and cols % group == 0,
-          f"cols = {cols} must be a multiple of 64 and of the group ({group}: 32, 64 or 128)")
+def _w4_buffers(codes, scales, rows, cols, group, index):
+    if group not in (32, 64, 128) or cols < 1 or cols % 64 or cols % group or rows < 1:
+        raise ValueError(f"a [{rows}][{cols}] layer in groups of {group}: cols must be a multiple of 64 and of the "
+                         "group, which is 32, 64 or 128")
     cs, ss = w4_shapes(rows, cols, group)
-    return _plane(codes, cs, torch.uint8, "codes"), _plane(scales, ss, _BF16, "scales")
+    return _plane(codes, cs, _U8, index, "codes"), _plane(scales, ss, _BF16, index, "scales")
 
 
 def ifq_w4_quantize(tensors, group, dev_status=None, stream=None):
     """tensors: list of (R float32 [rows][cols], codes uint8, scales bf16), the last two written, of w4_shapes()."""
-    arr = (W4Tensor * len(tensors))()
-    for i, (R, codes, scales) in enumerate(tensors):
+    index, words = tensors[0][0].get_device(), []
+    for R, codes, scales in tensors:
         rows, cols = R.shape
-        c, s = _w4_buffers(codes, scales, rows, cols, group)
-        arr[i] = W4Tensor(_plane(R, (rows, cols), torch.float32, "R"), rows, cols, c, s)
-    dev = _device_of([t for ts in tensors for t in ts] + [dev_status])
-    _enqueue(dev, stream, load().ifq_w4_quantize, arr, len(tensors), group, _ptr(dev_status))
+        c, s = _w4_buffers(codes, scales, rows, cols, group, index)
+        words += (_plane(R, (rows, cols), _F32, index, "R"), rows, cols, c, s)
+    _enqueue(index, stream, load().ifq_w4_quantize, (ctypes.c_int64 * len(words))(*words), len(tensors), group,
+             _status_ptr(dev_status, index))
 
 
 def ifq_w4_dequantize(tensors, group, stream=None):
     """tensors: list of (codes, scales, w bf16 [rows][cols]), w written."""
-    arr = (W4DqTensor * len(tensors))()
-    for i, (codes, scales, w) in enumerate(tensors):
+    index, words = tensors[0][0].get_device(), []
+    for codes, scales, w in tensors:
         rows, cols = w.shape
-        c, s = _w4_buffers(codes, scales, rows, cols, group)
-        arr[i] = W4DqTensor(c, s, rows, cols, _plane(w, (rows, cols), _BF16, "w"))
-    _enqueue(_device_of([t for ts in tensors for t in ts]), stream, load().ifq_w4_dequantize, arr, len(tensors), group)
+        c, s = _w4_buffers(codes, scales, rows, cols, group, index)
+        words += (c, s, rows, cols, _plane(w, (rows, cols), _BF16, index, "w"))
+    _enqueue(index, stream, load().ifq_w4_dequantize, (ctypes.c_int64 * len(words))(*words), len(tensors), group)
+
+
+def _w4_layers(layers, group, B):
+    """(device index, descriptor words) of ifq_w4_gemv's layers."""
+    index, words = layers[0]["codes"].get_device(), []
+    for d in layers:
+        rows, cols = d["rows"], d["cols"]
+        c, s = _w4_buffers(d["codes"], d["scales"], rows, cols, group, index)
+        x_im, y_im = d.get("x_im"), d.get("y_im")
+        if y_im is not None and rows % 2:
+            raise ValueError("planar outputs need an even number of rows")
+        xs = (B, cols if x_im is None else cols // 2)
+        ys = (B, rows if y_im is None else rows // 2)
+        words += (c, s, rows, cols, _plane(d["x_re"], xs, _BF16, index, "x_re"),
+                  0 if x_im is None else _plane(x_im, xs, _BF16, index, "x_im"),
+                  _plane(d["y_re"], ys, _F32, index, "y_re"),
+                  0 if y_im is None else _plane(y_im, ys, _F32, index, "y_im"))
+    return index, (ctypes.c_int64 * len(words))(*words)
+
+
+class W4LayerSet:
+    """Layers of ifq_w4_gemv checked and marshalled once for B tokens, for a caller that repeats the same call (the
+    tensors must stay alive and in place).  Accepted by ifq_w4_gemv in place of the list."""
+
+    def __init__(self, layers, group, B):
+        self.layers, self.group, self.B = list(layers), group, B
+        self.index, self.array = _w4_layers(self.layers, group, B)
 
 
 def ifq_w4_gemv(layers, group, B, dev_status=None, stream=None):
     """layers: list of dicts with codes, scales, rows, cols, x_re, x_im (bf16 [B][cols/2]; x_im None: x_re is
-    [B][cols]) and y_re, y_im (float32 [B][rows/2]; y_im None: y_re is [B][rows])."""
-    arr = (W4Layer * len(layers))()
-    for i, d in enumerate(layers):
-        rows, cols = d["rows"], d["cols"]
-        c, s = _w4_buffers(d["codes"], d["scales"], rows, cols, group)
-        x_im, y_im = d.get("x_im"), d.get("y_im")
-        _need(y_im is None or rows % 2 == 0, "planar outputs need an even number of rows")
-        xs = (B, cols // (1 if x_im is None else 2))
-        ys = (B, rows // (1 if y_im is None else 2))
-        arr[i] = W4Layer(c, s, rows, cols, _plane(d["x_re"], xs, _BF16, "x_re"),
-                         None if x_im is None else _plane(x_im, xs, _BF16, "x_im"),
-                         _plane(d["y_re"], ys, torch.float32, "y_re"),
-                         None if y_im is None else _plane(y_im, ys, torch.float32, "y_im"))
-    dev = _device_of([d.get(n) for d in layers for n in ("codes", "scales", "x_re", "x_im", "y_re", "y_im")] +
-                     [dev_status])
-    _enqueue(dev, stream, load().ifq_w4_gemv, arr, len(layers), group, B, _ptr(dev_status))
+    [B][cols]) and y_re, y_im (float32 [B][rows/2]; y_im None: y_re is [B][rows]), or a W4LayerSet of them."""
+    if isinstance(layers, W4LayerSet):
+        if layers.group != group or layers.B != B:
+            raise ValueError(f"the layers were marshalled for group {layers.group} and {layers.B} tokens")
+        index, arr, n = layers.index, layers.array, len(layers.layers)
+    else:
+        (index, arr), n = _w4_layers(layers, group, B), len(layers)
+    _enqueue(index, stream, load().ifq_w4_gemv, arr, n, group, B, _status_ptr(dev_status, index))
 
 
 class Kv4Cache:
@@ -457,68 +494,78 @@ class Kv4Cache:
     rows         rows of the q, k, v and o buffers (default B n_new)"""
 
     def __init__(self, records, page_table, kv_lens, dim, n_new=1, rows=None, new_offsets=None):
-        _need(records.dim() == 4 and records.shape[3] == 32 * dim + 256,
-              f"records must be [pages][kv_heads][page_tokens/16][{32 * dim + 256}]")
+        if records.dim() != 4 or records.shape[3] != 32 * dim + 256 or page_table.dim() != 2:
+            raise ValueError(f"needs records [pages][kv_heads][page_tokens/16][{32 * dim + 256}] and page_table "
+                             f"[B][table_cols], got {tuple(records.shape)} and {tuple(page_table.shape)}")
         pages, kv_heads, tiles = records.shape[:3]
         B = kv_lens.shape[0]
         self.dim, self.kv_heads, self.B, self.n_new = dim, kv_heads, B, n_new
         self.rows = B * n_new if rows is None else rows
         self._keep = (records, page_table, kv_lens, new_offsets)
-        self.device = _device_of(self._keep)
-        _need(page_table.dim() == 2, "page_table must be [B][table_cols]")
+        self.index = i = records.get_device()
         self.desc = Kv4CacheDesc(
-            _plane(records, records.shape, torch.uint8, "records"), pages, 16 * tiles, kv_heads, dim, B, n_new, self.rows,
-            _plane(page_table, (B, page_table.shape[1]), torch.int32, "page_table"), page_table.shape[1],
-            _plane(kv_lens, (B,), torch.int32, "kv_lens"),
-            None if new_offsets is None else _plane(new_offsets, (B + 1,), torch.int32, "new_offsets"))
+            _plane(records, tuple(records.shape), _U8, i, "records"), pages, 16 * tiles, kv_heads, dim, B, n_new,
+            self.rows, _plane(page_table, (B, page_table.shape[1]), _I32, i, "page_table"), page_table.shape[1],
+            _plane(kv_lens, (B,), _I32, i, "kv_lens"),
+            None if new_offsets is None else _plane(new_offsets, (B + 1,), _I32, i, "new_offsets"))
+        self._ref = ctypes.byref(self.desc)
 
     @staticmethod
     def records_shape(pages, kv_heads, page_tokens, dim):
         return pages, kv_heads, page_tokens // 16, 32 * dim + 256
 
 
-def _row_planes(cache, planes, width, dtype, what):
-    """Pointers and the common row stride of [rows][width] planes whose rows may be slices of wider ones."""
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    ld = planes[0].stride(0) if planes[0].shape[0] > 1 else max(width, planes[0].stride(0))
+def _row_planes(cache, planes, width, dtypes, what):
+    """Addresses and the common row stride of [rows][width] planes whose rows may be slices of wider ones."""
+    rows, index, ld = cache.rows, cache.index, None
     for t in planes:
-        _need(t.dtype in dtypes and t.dim() == 2 and t.shape[0] >= cache.rows and t.shape[1] == width and
-              t.stride(1) == 1 and (t.shape[0] == 1 or t.stride(0) == ld),
-              f"{what}: needs {dtypes[0]} [{cache.rows}][{width}] planes with one row stride")
-    _need(_device_of(planes) == cache.device, f"{what}: on another device than the cache")
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or t.dtype not in dtypes or t.stride(1) != 1:
+            raise ValueError(f"{what}: needs {dtypes[0]} planes [{rows}][{width}], rows contiguous; got {t.dtype} "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+        if t.get_device() != index:
+            raise ValueError(f"{what}: on {t.device}, the cache on cuda:{index}")
+        step = t.stride(0) if t.shape[0] > 1 else width   # a single row's stride says nothing
+        if ld is not None and step != ld:
+            raise ValueError(f"{what}: the planes' row strides differ ({ld} and {step})")
+        ld = step
     return [t.data_ptr() for t in planes], ld
 
 
 def ifq_kv4_append(cache, k_re, k_im, v_re, v_im, dev_status=None, stream=None):
     """Quantizes the new tokens' keys and values (float32 [rows][kv_heads dim], or column slices of wider
     buffers with one row stride) into the cache."""
-    p, ld = _row_planes(cache, (k_re, k_im, v_re, v_im), cache.kv_heads * cache.dim, torch.float32, "k, v")
-    _enqueue(cache.device, stream, load().ifq_kv4_append, ctypes.byref(cache.desc), *p, ld, _ptr(dev_status))
+    p, ld = _row_planes(cache, (k_re, k_im, v_re, v_im), cache.kv_heads * cache.dim, _F32, "k, v")
+    _enqueue(cache.index, stream, load().ifq_kv4_append, cache._ref, *p, ld, _status_ptr(dev_status, cache.index))
 
 
 def ifq_kv4_read(cache, k_re, k_im, v_re, v_im, dev_status=None, stream=None):
     """Writes the stored values of the new tokens (float32, laid out as for ifq_kv4_append)."""
-    p, ld = _row_planes(cache, (k_re, k_im, v_re, v_im), cache.kv_heads * cache.dim, torch.float32, "k, v")
-    _enqueue(cache.device, stream, load().ifq_kv4_read, ctypes.byref(cache.desc), *p, ld, _ptr(dev_status))
+    p, ld = _row_planes(cache, (k_re, k_im, v_re, v_im), cache.kv_heads * cache.dim, _F32, "k, v")
+    _enqueue(cache.index, stream, load().ifq_kv4_read, cache._ref, *p, ld, _status_ptr(dev_status, cache.index))
 
 
 def ifq_kv4_attention_workspace_bytes(cache, q_heads):
-    return int(load().ifq_kv4_attention_workspace_bytes(ctypes.byref(cache.desc), q_heads))
+    return int(load().ifq_kv4_attention_workspace_bytes(cache._ref, q_heads))
 
 
 def ifq_kv4_attention(cache, q_re, q_im, o_re, o_im, scale, workspace=None, dev_status=None, stream=None,
                       workspace_bytes=None):
     """q_re, q_im: float32 [rows][q_heads dim]; o_re, o_im: bf16, the same shape, written.  workspace: a device
     buffer of ifq_kv4_attention_workspace_bytes(cache, q_heads) bytes (no initial contents needed)."""
-    width = q_re.shape[1]
-    _need(width % cache.dim == 0, "q's row must be a whole number of heads")
-    q, ldq = _row_planes(cache, (q_re, q_im), width, torch.float32, "q")
+    width, index = q_re.shape[-1], cache.index
+    if width % cache.dim:
+        raise ValueError("q's row must be a whole number of heads")
+    q, ldq = _row_planes(cache, (q_re, q_im), width, _F32, "q")
     o, ldo = _row_planes(cache, (o_re, o_im), width, _BF16, "o")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    nbytes, ws = 0, None
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the cache's device")
+        nbytes, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     if workspace_bytes is not None:
         nbytes = workspace_bytes
-    _enqueue(cache.device, stream, load().ifq_kv4_attention, ctypes.byref(cache.desc), width // cache.dim, *q, ldq,
-             float(scale), *o, ldo, _ptr(workspace), nbytes, _ptr(dev_status))
+    _enqueue(index, stream, load().ifq_kv4_attention, cache._ref, width // cache.dim, *q, ldq, scale, *o, ldo, ws,
+             nbytes, _status_ptr(dev_status, index))
 
 
 # Raw entry point for callers that build ctypes descriptors themselves.
