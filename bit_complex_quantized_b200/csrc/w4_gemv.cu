@@ -84,35 +84,46 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
   // this CTA's columns, whole units
   const int64_t units = L.cols / U, per = (units + p.cluster - 1) / p.cluster;
   const int64_t kb = min(units, rank * per) * U, ke = min(units, (rank + 1) * per) * U;
-  const int nst = (int)((ke - kb + kStageCols - 1) / kStageCols);
 
-  auto load = [&](int st) {
-    if (st < nst) {
-      uint8_t* base = smem + (st % R::kStages) * R::kStage;
-      const int64_t k0 = kb + (int64_t)st * kStageCols;
-      const int tiles = (int)((min(ke, k0 + kStageCols) - k0) / 64);
+  // Sources of this thread's copies, moved on by a stage after each: its strips' codes and scales, and 8
+  // columns of the tokens warp + 8 i (in the first plane up to x_split, then in the second).
+  const uint8_t* code_src[MT];
+  const uint8_t* scale_src[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t strip = min(strip0 + m, strips - 1);   // rows past the layer repeat its last strip
+    code_src[m] = L.codes + (strip * (L.cols / 64) + kb / 64) * kQ4TileBytes + lane * 16;
+    scale_src[m] = reinterpret_cast<const uint8_t*>(L.scales) + (strip * (L.cols / G) + kb / G) * 32 + lane * 16;
+  }
+  int64_t xk = kb + lane * 8;
+  int64_t k_left = ke - kb;   // columns not yet asked for
+  int slot = 0;               // of the next load
+  auto load = [&]() {
+    if (k_left > 0) {
+      uint8_t* base = smem + slot * R::kStage;
+      const int tiles = k_left >= kStageCols ? kStageCols / 64 : (int)(k_left / 64);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        if (strip0 + m >= strips) break;
         uint8_t* c = base + (warp * MT + m) * R::kStripBytes + lane * 16;
-        const uint8_t* src = L.codes + ((strip0 + m) * (L.cols / 64) + k0 / 64) * kQ4TileBytes + lane * 16;
 #pragma unroll
         for (int i = 0; i < kStageCols / 64; ++i)
-          if (i < tiles) cp_async16(c + i * kQ4TileBytes, src + i * kQ4TileBytes);
+          if (i < tiles) cp_async16(c + i * kQ4TileBytes, code_src[m] + i * kQ4TileBytes);
         if (lane * 16 < tiles * 64 / G * 32)
-          cp_async16(base + R::kCodes + (warp * MT + m) * R::kScaleBytes + lane * 16,
-                     reinterpret_cast<const uint8_t*>(L.scales) + ((strip0 + m) * (L.cols / G) + k0 / G) * 32 + lane * 16);
+          cp_async16(base + R::kCodes + (warp * MT + m) * R::kScaleBytes + lane * 16, scale_src[m]);
+        code_src[m] += R::kStripBytes;
+        scale_src[m] += R::kScaleBytes;
       }
-      uint8_t* xs = base + R::kCodes + R::kScales;
-      for (int i = threadIdx.x; i < p.B * 32; i += kThreads) {  // token i / 32, 8 columns each
-        const int n = i >> 5, v = i & 31;
-        const int64_t k = k0 + v * 8;
-        if (k < ke) {
-          const int pl = k >= L.x_split;
-          const int64_t w = pl ? L.cols - L.x_split : L.x_split;
-          cp_async16(xs + (((v >> 2) * NT * 8 + n) * 4 + (v & 3)) * 16, L.x[pl] + n * w + (pl ? k - L.x_split : k));
-        }
-      }
+      uint8_t* xs = base + R::kCodes + R::kScales + ((lane >> 2) * NT * 32 + (lane & 3)) * 16;
+      const bool second = xk >= L.x_split;
+      const uint16_t* src = second ? L.x[1] + (xk - L.x_split) : L.x[0] + xk;
+      const int64_t width = second ? L.cols - L.x_split : L.x_split;
+      if (xk < ke)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          if (warp + 8 * i < p.B) cp_async16(xs + (warp + 8 * i) * 64, src + (warp + 8 * i) * width);
+      xk += kStageCols;
+      k_left -= kStageCols;
+      slot = slot + 1 == R::kStages ? 0 : slot + 1;
     }
     cp_async_commit();
   };
@@ -123,61 +134,70 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.0f;
 
-  for (int st = 0; st < R::kStages - 1; ++st) load(st);
-  for (int st = 0; st < nst; ++st) {
-    cp_async_wait<R::kStages - 2>();
-    __syncthreads();  // the stage's copies of every warp are in; the previous stage has been read
-    load(st + R::kStages - 1);
-    const uint8_t* base = smem + (st % R::kStages) * R::kStage;
+  // Columns of B past the last token repeat it (their results are dropped), so that no lane waits on a branch.
+  int x_off[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) x_off[nt] = (min(nt * 8 + g, p.B - 1) * 4 + t) * 16;
+
+  auto unit = [&](const uint8_t* base, int u) {
+    const uint8_t* cs = base + warp * MT * R::kStripBytes + lane * 16;
+    const uint8_t* ss = base + R::kCodes + warp * MT * R::kScaleBytes + g * 4;
     const uint8_t* xs = base + R::kCodes + R::kScales;
-    const int us = (int)((min(ke, kb + (int64_t)(st + 1) * kStageCols) - kb - (int64_t)st * kStageCols) / U);
+    float part[MT][NT][4];
 #pragma unroll
-    for (int u = 0; u < kStageCols / U; ++u) {
-      if (u >= us) break;
-      float part[MT][NT][4];
+    for (int i = 0; i < U / 64; ++i) {
+      const int tl = u * (U / 64) + i;
+      uint4 w4[MT];
 #pragma unroll
-      for (int i = 0; i < U / 64; ++i) {
-        const int tl = u * (U / 64) + i;
-        uint4 w4[MT];
+      for (int m = 0; m < MT; ++m)
+        w4[m] = *reinterpret_cast<const uint4*>(cs + m * R::kStripBytes + tl * kQ4TileBytes);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          w4[m] = *reinterpret_cast<const uint4*>(base + (warp * MT + m) * R::kStripBytes + tl * kQ4TileBytes + lane * 16);
+      for (int c = 0; c < 2; ++c) {
+        const int ch = tl * 2 + c;
+        uint4 b[NT];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int ch = tl * 2 + c;
-          uint4 b[NT];
+        for (int nt = 0; nt < NT; ++nt) b[nt] = *reinterpret_cast<const uint4*>(xs + ch * NT * 512 + x_off[nt]);
+        const bool first = (64 * i + 32 * c) % G == 0, last = (64 * i + 32 * c + 32) % G == 0;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t lo[4], hi[4];
+          q4_expand<kQ4Sub8>(c ? w4[m].z : w4[m].x, lo);
+          q4_expand<kQ4Sub8>(c ? w4[m].w : w4[m].y, hi);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            b[nt] = make_uint4(0, 0, 0, 0);
-            if (nt * 8 + g < p.B)
-              b[nt] = *reinterpret_cast<const uint4*>(xs + ((ch * NT * 8 + nt * 8 + g) * 4 + t) * 16);
+            if (first) mma_bf16_first(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
+            else mma_bf16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
+            mma_bf16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
           }
-          const bool first = (64 * i + 32 * c) % G == 0, last = (64 * i + 32 * c + 32) % G == 0;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t lo[4], hi[4];
-            q4_expand<kQ4Sub8>(c ? w4[m].z : w4[m].x, lo);
-            q4_expand<kQ4Sub8>(c ? w4[m].w : w4[m].y, hi);
+          if (last) {
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(ss + m * R::kScaleBytes + (ch * 32 / G) * 32);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              if (first) part[m][nt][0] = part[m][nt][1] = part[m][nt][2] = part[m][nt][3] = 0.0f;
-              mma_bf16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
-              mma_bf16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
-            }
-            if (last) {
-              const uint32_t sc = *reinterpret_cast<const uint32_t*>(base + R::kCodes + (warp * MT + m) * R::kScaleBytes +
-                                                                     (ch * 32 / G) * 32 + g * 4);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                acc[m][nt][0] = fmaf(bf16_lo(sc), part[m][nt][0], acc[m][nt][0]);
-                acc[m][nt][1] = fmaf(bf16_lo(sc), part[m][nt][1], acc[m][nt][1]);
-                acc[m][nt][2] = fmaf(bf16_hi(sc), part[m][nt][2], acc[m][nt][2]);
-                acc[m][nt][3] = fmaf(bf16_hi(sc), part[m][nt][3], acc[m][nt][3]);
-              }
+              acc[m][nt][0] = fmaf(bf16_lo(sc), part[m][nt][0], acc[m][nt][0]);
+              acc[m][nt][1] = fmaf(bf16_lo(sc), part[m][nt][1], acc[m][nt][1]);
+              acc[m][nt][2] = fmaf(bf16_hi(sc), part[m][nt][2], acc[m][nt][2]);
+              acc[m][nt][3] = fmaf(bf16_hi(sc), part[m][nt][3], acc[m][nt][3]);
             }
           }
         }
       }
+    }
+  };
+
+#pragma unroll
+  for (int st = 0; st < R::kStages - 1; ++st) load();
+  int at = 0;  // slot of the stage being read
+  for (int64_t left = ke - kb; left > 0; left -= kStageCols) {
+    cp_async_wait<R::kStages - 2>();
+    __syncthreads();  // the stage's copies of every warp are in; the previous stage has been read
+    load();
+    const uint8_t* base = smem + at * R::kStage;
+    at = at + 1 == R::kStages ? 0 : at + 1;
+    if (left >= kStageCols) {
+#pragma unroll
+      for (int u = 0; u < kStageCols / U; ++u) unit(base, u);
+    } else {
+      for (int u = 0; u < (int)(left / U); ++u) unit(base, u);
     }
   }
   cp_async_wait<0>();
