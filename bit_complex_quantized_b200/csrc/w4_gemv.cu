@@ -5,20 +5,24 @@
 // (q4_common.cuh), x is the B operand as it is, so all products are exact and a group accumulates
 // in float32; the group's scale multiplies that sum in float32.
 //
-// HBM-bound by the codes.  A CTA of 8 warps takes 128 kMT rows (16 kMT per warp) x a slice of the
-// columns, 256 columns a stage, through a ring of asynchronous copies: codes and scales are contiguous
-// runs private to a warp, the stage's x is shared by the CTA (one barrier a stage).  A layer with few row
-// tiles has its columns split over a cluster, whose CTAs add their sums through distributed
-// shared memory in rank order: one launch, no workspace, a fixed order of sums.
+// HBM-bound by the codes.  A CTA of 4 warps takes 128 rows x a slice of the columns; its warps take
+// the slice's 64-column tiles in turn, each for all 128 rows, so that a tile's x is read from
+// shared memory once for all strips, nothing is shared between warps, and the loop has no
+// barrier: every warp runs its own ring of asynchronous copies (codes, scales, x of one tile a stage).
+// The warps' sums are added in shared memory at the end, and where a layer has few row tiles its
+// columns are split over a cluster, whose CTAs add theirs through distributed shared memory: one launch,
+// no workspace, a fixed order of sums.
 #include "ifq_internal.h"
 #include "q4_common.cuh"
 
 namespace ifq {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStageCols = 256;
+constexpr int kStrips = 4;                 // 16-row strips of a CTA
+constexpr int kRows = kStrips * 16;
+constexpr int kCols = 128;                 // of a stage: two tiles
 constexpr int kMaxCluster = 8;
 
 struct LArg {
@@ -26,9 +30,12 @@ struct LArg {
   const uint16_t* scales;
   const uint16_t* x[2];
   float* y[2];
-  int64_t rows, cols;
+  int64_t rows;
   int64_t x_split, y_split;  // first column / row of the second plane (cols / rows where there is none)
-  int64_t tile_begin;        // first row tile of the layer in the call
+  int32_t cols;
+  int32_t cluster_begin;     // first cluster of the layer in the call
+  int32_t split;             // CTAs that share a row tile's columns: 1 .. cluster size, a power of two
+  int32_t tiles;             // row tiles
 };
 
 template <int kCap>
@@ -38,17 +45,20 @@ struct LParams {
   uint32_t* status;
 };
 
-template <int G, int NT, int MT>
+// A warp's stage: two 64-column tiles of all strips, their scales and the x of up to XB tokens.
+template <int G, int XB>
 struct Ring {
-  static constexpr int kScaleBytes = kStageCols / G * 32;               // of a strip of 16 rows
-  static constexpr int kStripBytes = kStageCols / 64 * kQ4TileBytes;    // codes of a strip
-  static constexpr int kCodes = kWarps * MT * kStripBytes;
-  static constexpr int kScales = kWarps * MT * kScaleBytes;
-  static constexpr int kX = kStageCols / 32 * NT * 8 * 64;
+  static constexpr int NT = (XB + 7) / 8;
+  static constexpr int kStripBytes = 2 * kQ4TileBytes;
+  static constexpr int kScaleBytes = kCols / G * 32;                    // of a strip
+  static constexpr int kCodes = kStrips * kStripBytes;
+  static constexpr int kScales = kStrips * kScaleBytes;
+  static constexpr int kX = XB * kCols * 2;
   static constexpr int kStage = kCodes + kScales + kX;
-  static constexpr int kStages = 4;
-  static constexpr int kBytes = kStages * kStage;
-  static_assert(kBytes >= kWarps * MT * 16 * NT * 8 * 4, "the sums reuse the ring");
+  static constexpr int kStages = 2;
+  static constexpr int kBytes = kWarps * kStages * kStage;
+  static constexpr int kCtas = 227 * 1024 / (kBytes + 1024);            // that an SM holds
+  static_assert(kBytes >= kWarps * kRows * XB * 4, "the sums reuse the ring");
 };
 
 IFQ_DEVINL uint32_t cluster_rank() {
@@ -67,117 +77,122 @@ IFQ_DEVINL float ld_cluster(const void* smem, uint32_t rank) {
   return v;
 }
 
-template <int G, int NT, int MT, int kCap>
+template <int G, int XB, int kCap>
 __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant__ LParams<kCap> p) {
-  using R = Ring<G, NT, MT>;
-  constexpr int U = G > 64 ? G : 64;
-  constexpr int kRows = kWarps * MT * 16;
+  using R = Ring<G, XB>;
+  constexpr int NT = R::NT;
   extern __shared__ __align__(128) uint8_t smem[];
   const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
-  const int64_t tile = (int64_t)blockIdx.x / p.cluster;
+  const int cl = (int)blockIdx.x / p.cluster;
   int li = 0;
-  while (li + 1 < p.count && tile >= p.l[li + 1].tile_begin) ++li;
+  while (li + 1 < p.count && cl >= p.l[li + 1].cluster_begin) ++li;
   const LArg& L = p.l[li];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t row0 = (tile - L.tile_begin) * kRows;
-  const int64_t strips = (L.rows + 15) / 16, strip0 = row0 / 16 + warp * MT;
-  // this CTA's columns, whole units
-  const int64_t units = L.cols / U, per = (units + p.cluster - 1) / p.cluster;
-  const int64_t kb = min(units, rank * per) * U, ke = min(units, (rank + 1) * per) * U;
+  // this CTA's rows, and its columns [kb, ke) in whole stages; this warp's stages are warp, + kWarps, ...
+  const int sub = rank % L.split;
+  const int tile = (cl - L.cluster_begin) * (p.cluster / L.split) + rank / L.split;
+  const int64_t row0 = (int64_t)tile * kRows;
+  const int units = (L.cols + kCols - 1) / kCols, per = (units + L.split - 1) / L.split;
+  const int kb = min(units, sub * per) * kCols, ke = tile < L.tiles ? min(L.cols, kb + per * kCols) : kb;
+  const int k_first = kb + warp * kCols;
 
-  // Sources of this thread's copies, moved on by a stage after each: its strips' codes and scales, and 8
-  // columns of the tokens warp + 8 i (in the first plane up to x_split, then in the second).
-  const uint8_t* code_src[MT];
-  const uint8_t* scale_src[MT];
+  // Sources of this lane's copies, moved on to the warp's next stage after each.  Strips past the layer repeat its
+  // last one.
+  const int64_t strips = (L.rows + 15) / 16;
+  const uint8_t* code_src[kStrips];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t strip = min(strip0 + m, strips - 1);   // rows past the layer repeat its last strip
-    code_src[m] = L.codes + (strip * (L.cols / 64) + kb / 64) * kQ4TileBytes + lane * 16;
-    scale_src[m] = reinterpret_cast<const uint8_t*>(L.scales) + (strip * (L.cols / G) + kb / G) * 32 + lane * 16;
-  }
-  int64_t xk = kb + lane * 8;
-  int64_t k_left = ke - kb;   // columns not yet asked for
-  int slot = 0;               // of the next load
-  auto load = [&]() {
-    if (k_left > 0) {
-      uint8_t* base = smem + slot * R::kStage;
-      const int tiles = k_left >= kStageCols ? kStageCols / 64 : (int)(k_left / 64);
+  for (int m = 0; m < kStrips; ++m)
+    code_src[m] = L.codes + min(strips - 1, row0 / 16 + m) * (L.cols * 8ll) + k_first * 8ll + lane * 16;
+  constexpr int kLanes = R::kScaleBytes / 16;                 // lanes that fetch a strip's scales
+  const uint8_t* scale_src = reinterpret_cast<const uint8_t*>(L.scales) +
+                             min(strips - 1, row0 / 16 + lane / kLanes) * (L.cols / G * 32ll) + k_first / G * 32 +
+                             (lane % kLanes) * 16;
+  const int xt = lane >> 4, xv = lane & 15;                   // 8 columns of the tokens xt + 2 i
+  int xk = k_first + xv * 8;
+  bool second = xk >= L.x_split;
+  const uint16_t* x_src = second ? L.x[1] + xt * (L.cols - L.x_split) + (xk - L.x_split) : L.x[0] + xt * L.x_split + xk;
+  int64_t x_step = 2 * (second ? L.cols - L.x_split : L.x_split);
+  const uint32_t ring = smem_u32(smem) + warp * R::kStages * R::kStage;
+  const uint32_t code_dst = ring + lane * 16, scale_dst = ring + R::kCodes + lane * 16;
+  const uint32_t x_dst = ring + R::kCodes + R::kScales + ((xv >> 2) * XB * 4 + (xv & 3)) * 16 + xt * 64;
+  int kl = k_first;   // columns of the next load
+  auto load = [&](int slot) {
+    if (kl < ke) {
+      const bool whole = kl + kCols <= ke;  // a layer's last stage may be one tile
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint8_t* c = base + (warp * MT + m) * R::kStripBytes + lane * 16;
-#pragma unroll
-        for (int i = 0; i < kStageCols / 64; ++i)
-          if (i < tiles) cp_async16(c + i * kQ4TileBytes, code_src[m] + i * kQ4TileBytes);
-        if (lane * 16 < tiles * 64 / G * 32)
-          cp_async16(base + R::kCodes + (warp * MT + m) * R::kScaleBytes + lane * 16, scale_src[m]);
-        code_src[m] += R::kStripBytes;
-        scale_src[m] += R::kScaleBytes;
+      for (int m = 0; m < kStrips; ++m) {
+        cp_async16(code_dst + slot * R::kStage + m * R::kStripBytes, code_src[m]);
+        if (whole) cp_async16(code_dst + slot * R::kStage + m * R::kStripBytes + kQ4TileBytes, code_src[m] + kQ4TileBytes);
+        code_src[m] += kWarps * R::kStripBytes;
       }
-      uint8_t* xs = base + R::kCodes + R::kScales + ((lane >> 2) * NT * 32 + (lane & 3)) * 16;
-      const bool second = xk >= L.x_split;
-      const uint16_t* src = second ? L.x[1] + (xk - L.x_split) : L.x[0] + xk;
-      const int64_t width = second ? L.cols - L.x_split : L.x_split;
-      if (xk < ke)
+      if (lane < kStrips * kLanes && (whole || (lane % kLanes) * 16 < 64 / G * 32))
+        cp_async16(scale_dst + slot * R::kStage, scale_src);
+      scale_src += kWarps * R::kScaleBytes;
+      if (xk < ke) {
+        const uint16_t* src = x_src;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (warp + 8 * i < p.B) cp_async16(xs + (warp + 8 * i) * 64, src + (warp + 8 * i) * width);
-      xk += kStageCols;
-      k_left -= kStageCols;
-      slot = slot + 1 == R::kStages ? 0 : slot + 1;
+        for (int i = 0; i < (XB + 1) / 2; ++i) {
+          if (2 * i >= p.B) break;
+          if (xt + 2 * i < p.B) cp_async16(x_dst + slot * R::kStage + i * 128, src);
+          src += x_step;
+        }
+      }
+      kl += kWarps * kCols;
+      xk += kWarps * kCols;
+      x_src += kWarps * kCols;
+      if (!second && xk >= L.x_split) {
+        second = true;
+        x_src = L.x[1] + xt * (L.cols - L.x_split) + (xk - L.x_split);
+        x_step = 2 * (L.cols - L.x_split);
+      }
     }
     cp_async_commit();
   };
 
-  float acc[MT][NT][4];
+  float acc[kStrips][NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < kStrips; ++m)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.0f;
-
   // Columns of B past the last token repeat it (their results are dropped), so that no lane waits on a branch.
-  int x_off[NT];
+  const uint8_t* base0 = smem + warp * R::kStages * R::kStage;
+  const uint8_t* xs[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) x_off[nt] = (min(nt * 8 + g, p.B - 1) * 4 + t) * 16;
+  for (int nt = 0; nt < NT; ++nt)
+    xs[nt] = base0 + R::kCodes + R::kScales + (min(nt * 8 + g, p.B - 1) * 4 + t) * 16;
 
-  auto unit = [&](const uint8_t* base, int u) {
-    const uint8_t* cs = base + warp * MT * R::kStripBytes + lane * 16;
-    const uint8_t* ss = base + R::kCodes + warp * MT * R::kScaleBytes + g * 4;
-    const uint8_t* xs = base + R::kCodes + R::kScales;
-    float part[MT][NT][4];
+  auto tile_product = [&](int slot, int i) {
+    uint4 b[2][NT];
 #pragma unroll
-    for (int i = 0; i < U / 64; ++i) {
-      const int tl = u * (U / 64) + i;
-      uint4 w4[MT];
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        w4[m] = *reinterpret_cast<const uint4*>(cs + m * R::kStripBytes + tl * kQ4TileBytes);
+      for (int nt = 0; nt < NT; ++nt)
+        b[c][nt] = *reinterpret_cast<const uint4*>(xs[nt] + slot * R::kStage + (2 * i + c) * XB * 64);
+#pragma unroll
+    for (int m = 0; m < kStrips; ++m) {
+      const uint4 w4 = *reinterpret_cast<const uint4*>(base0 + lane * 16 + slot * R::kStage + m * R::kStripBytes +
+                                                       i * kQ4TileBytes);
+      float part[NT][4];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int ch = tl * 2 + c;
-        uint4 b[NT];
+        uint32_t lo[4], hi[4];
+        q4_expand<kQ4Sub8>(c ? w4.z : w4.x, lo);
+        q4_expand<kQ4Sub8>(c ? w4.w : w4.y, hi);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) b[nt] = *reinterpret_cast<const uint4*>(xs + ch * NT * 512 + x_off[nt]);
-        const bool first = (64 * i + 32 * c) % G == 0, last = (64 * i + 32 * c + 32) % G == 0;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t lo[4], hi[4];
-          q4_expand<kQ4Sub8>(c ? w4[m].z : w4[m].x, lo);
-          q4_expand<kQ4Sub8>(c ? w4[m].w : w4[m].y, hi);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (c == 0 || G == 32) mma_bf16_first(part[nt], lo[0], hi[0], lo[1], hi[1], b[c][nt].x, b[c][nt].y);
+          else mma_bf16(part[nt], lo[0], hi[0], lo[1], hi[1], b[c][nt].x, b[c][nt].y);
+          mma_bf16(part[nt], lo[2], hi[2], lo[3], hi[3], b[c][nt].z, b[c][nt].w);
+        }
+        if (c == 1 || G == 32) {
+          const uint32_t sc = *reinterpret_cast<const uint32_t*>(base0 + g * 4 + slot * R::kStage + R::kCodes +
+                                                                 m * R::kScaleBytes + (64 * i + 32 * c) / G * 32);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (first) mma_bf16_first(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
-            else mma_bf16(part[m][nt], lo[0], hi[0], lo[1], hi[1], b[nt].x, b[nt].y);
-            mma_bf16(part[m][nt], lo[2], hi[2], lo[3], hi[3], b[nt].z, b[nt].w);
-          }
-          if (last) {
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(ss + m * R::kScaleBytes + (ch * 32 / G) * 32);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              acc[m][nt][0] = fmaf(bf16_lo(sc), part[m][nt][0], acc[m][nt][0]);
-              acc[m][nt][1] = fmaf(bf16_lo(sc), part[m][nt][1], acc[m][nt][1]);
-              acc[m][nt][2] = fmaf(bf16_hi(sc), part[m][nt][2], acc[m][nt][2]);
-              acc[m][nt][3] = fmaf(bf16_hi(sc), part[m][nt][3], acc[m][nt][3]);
-            }
+            acc[m][nt][0] = fmaf(bf16_lo(sc), part[nt][0], acc[m][nt][0]);
+            acc[m][nt][1] = fmaf(bf16_lo(sc), part[nt][1], acc[m][nt][1]);
+            acc[m][nt][2] = fmaf(bf16_hi(sc), part[nt][2], acc[m][nt][2]);
+            acc[m][nt][3] = fmaf(bf16_hi(sc), part[nt][3], acc[m][nt][3]);
           }
         }
       }
@@ -185,48 +200,52 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
   };
 
 #pragma unroll
-  for (int st = 0; st < R::kStages - 1; ++st) load();
-  int at = 0;  // slot of the stage being read
-  for (int64_t left = ke - kb; left > 0; left -= kStageCols) {
-    cp_async_wait<R::kStages - 2>();
-    __syncthreads();  // the stage's copies of every warp are in; the previous stage has been read
-    load();
-    const uint8_t* base = smem + at * R::kStage;
-    at = at + 1 == R::kStages ? 0 : at + 1;
-    if (left >= kStageCols) {
+  for (int st = 0; st < R::kStages - 1; ++st) load(st);
+  for (int k = k_first; k < ke;) {
 #pragma unroll
-      for (int u = 0; u < kStageCols / U; ++u) unit(base, u);
-    } else {
-      for (int u = 0; u < (int)(left / U); ++u) unit(base, u);
+    for (int slot = 0; slot < R::kStages; ++slot, k += kWarps * kCols) {
+      if (k >= ke) break;
+      cp_async_wait<R::kStages - 2>();
+      __syncwarp();  // every lane's copies of the stage are in, and the previous stage has been read
+      load((slot + R::kStages - 1) % R::kStages);
+      tile_product(slot, 0);
+      if (k + kCols <= ke) tile_product(slot, 1);
     }
   }
   cp_async_wait<0>();
   __syncthreads();
 
-  // sums[n][row] in the ring's memory, then over the cluster
+  // sums[warp][n][row] in the ring's memory; added over the warps, then over the cluster
   float* sums = reinterpret_cast<float*>(smem);
+  const int plane = p.B * kRows;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < kStrips; ++m)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int n = nt * 8 + 2 * t + (e & 1);
-        if (n < p.B) sums[n * kRows + (warp * MT + m) * 16 + g + 8 * (e >> 1)] = acc[m][nt][e];
+        if (n < p.B) sums[warp * plane + n * kRows + m * 16 + g + 8 * (e >> 1)] = acc[m][nt][e];
       }
-  if (p.cluster > 1) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
+  if (p.cluster > 1) {
+    for (int i = threadIdx.x; i < plane; i += kThreads)
+      sums[i] = (sums[i] + sums[plane + i]) + (sums[2 * plane + i] + sums[3 * plane + i]);
+    cluster_sync();
+  }
   bool bad = false;
-  const int span = kRows / p.cluster;
+  const int span = kRows / L.split;
   for (int i = threadIdx.x; i < p.B * span; i += kThreads) {
-    const int n = i / span, lr = rank * span + i % span;
+    const int n = i / span, lr = sub * span + i % span;
     const int64_t r = row0 + lr;
     if (r >= L.rows) continue;
-    float v = 0.0f;
-    if (p.cluster > 1) {
-      for (int k = 0; k < p.cluster; ++k) v += ld_cluster(sums + n * kRows + lr, k);
+    float v;
+    const float* at = sums + n * kRows + lr;
+    if (L.split > 1) {
+      v = 0.0f;
+      for (int k = 0; k < L.split; ++k) v += ld_cluster(at, rank - sub + k);
     } else {
-      v = sums[n * kRows + lr];
+      v = p.cluster > 1 ? at[0] : (at[0] + at[plane]) + (at[2 * plane] + at[3 * plane]);
     }
     v *= kQ4Unit;
     bad |= !(fabsf(v) <= 3.402823466e38f);
@@ -249,26 +268,63 @@ cudaError_t allow_smem(K kernel, int bytes, uint64_t* done) {
   return e;
 }
 
-template <int G, int NT, int MT, int kCap>
+template <int G, int XB, int kCap>
 cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_status, cudaStream_t s) {
-  using R = Ring<G, NT, MT>;
+  using R = Ring<G, XB>;
   static uint64_t done = 0;
-  auto kernel = w4_gemv_kernel<G, NT, MT, kCap>;
+  auto kernel = w4_gemv_kernel<G, XB, kCap>;
   cudaError_t err = allow_smem(kernel, R::kBytes, &done);
   if (err != cudaSuccess) return err;
-  LParams<kCap> p;
-  p.count = count;
-  p.B = B;
-  p.status = dev_status;
-  constexpr int kRows = kWarps * MT * 16;
-  // the layers with the longest rows first, so that the last CTAs to start are short ones
+  auto stages = [&](int i, int split) {  // of one CTA of layer i
+    return (Ls[i].cols / kCols + split * kWarps) / (split * kWarps);
+  };
+  auto tiles = [&](int i) { return (Ls[i].rows + kRows - 1) / kRows; };
+  // How far to split the columns.  Halving the longest slice helps while CTAs are few or long ones end last, and
+  // costs each CTA its start and join (kStart stages' time): the least of (work per slot) + (longest slice).
+  constexpr int kStart = 20;
+  int split[kCap], best = 0;
+  double best_cost = 0.0;
+  int64_t longest = 0;
+  for (int i = 0; i < count; ++i) longest = stages(i, 1) > longest ? stages(i, 1) : longest;
+  auto split_for = [&](int i, int64_t len) {
+    int sp = 1;
+    while (sp < kMaxCluster && stages(i, sp) > len) sp *= 2;
+    return sp;
+  };
+  for (int q = 1; q <= kMaxCluster; q *= 2) {
+    const int64_t len = (longest + q - 1) / q;
+    double work = 0.0;
+    int64_t top = 0;
+    for (int i = 0; i < count; ++i) {
+      const int sp = split_for(i, len);
+      const int64_t st = stages(i, sp);
+      work += (double)(tiles(i) * sp) * (double)(st + kStart);
+      top = st > top ? st : top;
+    }
+    const double cost = work / (148.0 * R::kCtas) + 0.5 * (double)(top + kStart);
+    if (best == 0 || cost < best_cost) {
+      best = q;
+      best_cost = cost;
+    }
+  }
+  int cluster = 1;
+  for (int i = 0; i < count; ++i) {
+    split[i] = split_for(i, (longest + best - 1) / best);
+    cluster = split[i] > cluster ? split[i] : cluster;
+  }
+  // the longest slices first, so that the last CTAs to start are short ones
   int order[kCap];
   for (int i = 0; i < count; ++i) {
     int j = i;
-    for (; j > 0 && Ls[order[j - 1]].cols < Ls[i].cols; --j) order[j] = order[j - 1];
+    for (; j > 0 && stages(order[j - 1], split[order[j - 1]]) < stages(i, split[i]); --j) order[j] = order[j - 1];
     order[j] = i;
   }
-  int64_t tiles = 0;
+  LParams<kCap> p;
+  p.count = count;
+  p.B = B;
+  p.cluster = cluster;
+  p.status = dev_status;
+  int64_t clusters = 0;
   for (int i = 0; i < count; ++i) {
     const ifq_w4_layer& a = Ls[order[i]];
     LArg& l = p.l[i];
@@ -279,17 +335,17 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
     l.y[0] = a.y_re;
     l.y[1] = a.y_im;
     l.rows = a.rows;
-    l.cols = a.cols;
+    l.cols = (int32_t)a.cols;
     l.x_split = a.x_im ? a.cols / 2 : a.cols;
     l.y_split = a.y_im ? a.rows / 2 : a.rows;
-    l.tile_begin = tiles;
-    tiles += (a.rows + kRows - 1) / kRows;
+    l.split = split[order[i]];
+    l.tiles = (int32_t)tiles(order[i]);
+    l.cluster_begin = (int32_t)clusters;
+    const int64_t each = cluster / l.split;  // row tiles of a cluster
+    clusters += (l.tiles + each - 1) / each;
   }
-  int cluster = 1;
-  while (cluster < kMaxCluster && tiles * cluster < 148 * 2) cluster *= 2;
-  p.cluster = cluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * cluster));
+  cfg.gridDim = dim3((unsigned)(clusters * cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = R::kBytes;
   cfg.stream = s;
@@ -304,8 +360,9 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
 
 template <int G, int kCap>
 cudaError_t by_batch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_status, cudaStream_t s) {
-  if (B <= 8) return launch<G, 1, 1, kCap>(Ls, count, B, dev_status, s);
-  return launch<G, 2, 2, kCap>(Ls, count, B, dev_status, s);
+  if (B <= 2) return launch<G, 2, kCap>(Ls, count, B, dev_status, s);
+  if (B <= 8) return launch<G, 8, kCap>(Ls, count, B, dev_status, s);
+  return launch<G, 16, kCap>(Ls, count, B, dev_status, s);
 }
 
 template <int G>
