@@ -7,6 +7,7 @@ there is no fallback: if libifq.so is missing, loading fails loudly.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -365,7 +366,7 @@ def ifq_gemm_wait_limit(layers, T, M, wait_limit_ns, dev_status=None, stream=Non
 
 # ------------------------------------------------------------------ 4-bit layers and cache
 # A decode step makes these calls every few microseconds of GPU time, so the checks build no message and no
-# object unless they fail, and descriptors are flat arrays of 64-bit words.
+# object unless they fail, and descriptors are packed as 64-bit words.
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 values or their bit patterns
 _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
@@ -389,14 +390,19 @@ def _enqueue(index, stream, fn, *args):
         _check(status)
 
 
-def _plane(t, shape, dtypes, index, what):
-    """Address of a contiguous tensor of the given shape and type on CUDA device `index` (None: any one)."""
-    if tuple(t.shape) != shape or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{what}: needs a contiguous {dtypes[0]} tensor of shape {shape}, got {t.dtype} "
+def _plane(t, numel, dtypes, index, what):
+    """Address of a contiguous tensor of `numel` elements and one of the types on CUDA device `index`."""
+    if t.numel() != numel or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{what}: needs a contiguous {dtypes[0]} tensor of {numel} elements, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     if t.get_device() != index or index < 0:
         raise ValueError(f"{what}: all tensors of a call must be on one CUDA device, got {t.device}")
     return t.data_ptr()
+
+
+def _words(words):
+    """An array of descriptors made of 64-bit words."""
+    return struct.pack(f"{len(words)}q", *words)
 
 
 def _status_ptr(t, index):
@@ -418,8 +424,9 @@ def _w4_buffers(codes, scales, rows, cols, group, index):
     if group not in (32, 64, 128) or cols < 1 or cols % 64 or cols % group or rows < 1:
         raise ValueError(f"a [{rows}][{cols}] layer in groups of {group}: cols must be a multiple of 64 and of the "
                          "group, which is 32, 64 or 128")
-    cs, ss = w4_shapes(rows, cols, group)
-    return _plane(codes, cs, _U8, index, "codes"), _plane(scales, ss, _BF16, index, "scales")
+    entries = (rows + 15) // 16 * 16 * cols
+    return (_plane(codes, entries // 2, _U8, index, "codes"),
+            _plane(scales, entries // group, _BF16, index, "scales"))
 
 
 def ifq_w4_quantize(tensors, group, dev_status=None, stream=None):
@@ -428,8 +435,8 @@ def ifq_w4_quantize(tensors, group, dev_status=None, stream=None):
     for R, codes, scales in tensors:
         rows, cols = R.shape
         c, s = _w4_buffers(codes, scales, rows, cols, group, index)
-        words += (_plane(R, (rows, cols), _F32, index, "R"), rows, cols, c, s)
-    _enqueue(index, stream, load().ifq_w4_quantize, (ctypes.c_int64 * len(words))(*words), len(tensors), group,
+        words += (_plane(R, rows * cols, _F32, index, "R"), rows, cols, c, s)
+    _enqueue(index, stream, load().ifq_w4_quantize, _words(words), len(tensors), group,
              _status_ptr(dev_status, index))
 
 
@@ -439,8 +446,8 @@ def ifq_w4_dequantize(tensors, group, stream=None):
     for codes, scales, w in tensors:
         rows, cols = w.shape
         c, s = _w4_buffers(codes, scales, rows, cols, group, index)
-        words += (c, s, rows, cols, _plane(w, (rows, cols), _BF16, index, "w"))
-    _enqueue(index, stream, load().ifq_w4_dequantize, (ctypes.c_int64 * len(words))(*words), len(tensors), group)
+        words += (c, s, rows, cols, _plane(w, rows * cols, _BF16, index, "w"))
+    _enqueue(index, stream, load().ifq_w4_dequantize, _words(words), len(tensors), group)
 
 
 def _w4_layers(layers, group, B):
@@ -452,13 +459,13 @@ def _w4_layers(layers, group, B):
         x_im, y_im = d.get("x_im"), d.get("y_im")
         if y_im is not None and rows % 2:
             raise ValueError("planar outputs need an even number of rows")
-        xs = (B, cols if x_im is None else cols // 2)
-        ys = (B, rows if y_im is None else rows // 2)
+        xs = B * (cols if x_im is None else cols // 2)
+        ys = B * (rows if y_im is None else rows // 2)
         words += (c, s, rows, cols, _plane(d["x_re"], xs, _BF16, index, "x_re"),
                   0 if x_im is None else _plane(x_im, xs, _BF16, index, "x_im"),
                   _plane(d["y_re"], ys, _F32, index, "y_re"),
                   0 if y_im is None else _plane(y_im, ys, _F32, index, "y_im"))
-    return index, (ctypes.c_int64 * len(words))(*words)
+    return index, _words(words)
 
 
 class W4LayerSet:
@@ -504,10 +511,10 @@ class Kv4Cache:
         self._keep = (records, page_table, kv_lens, new_offsets)
         self.index = i = records.get_device()
         self.desc = Kv4CacheDesc(
-            _plane(records, tuple(records.shape), _U8, i, "records"), pages, 16 * tiles, kv_heads, dim, B, n_new,
-            self.rows, _plane(page_table, (B, page_table.shape[1]), _I32, i, "page_table"), page_table.shape[1],
-            _plane(kv_lens, (B,), _I32, i, "kv_lens"),
-            None if new_offsets is None else _plane(new_offsets, (B + 1,), _I32, i, "new_offsets"))
+            _plane(records, records.numel(), _U8, i, "records"), pages, 16 * tiles, kv_heads, dim, B, n_new,
+            self.rows, _plane(page_table, B * page_table.shape[1], _I32, i, "page_table"), page_table.shape[1],
+            _plane(kv_lens, B, _I32, i, "kv_lens"),
+            None if new_offsets is None else _plane(new_offsets, B + 1, _I32, i, "new_offsets"))
         self._ref = ctypes.byref(self.desc)
 
     @staticmethod

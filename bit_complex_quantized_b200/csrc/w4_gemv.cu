@@ -23,7 +23,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStrips = 4;                 // 16-row strips of a CTA
 constexpr int kRows = kStrips * 16;
 constexpr int kCols = 128;                 // of a stage: two tiles
-constexpr int kMaxCluster = 8;
+constexpr int kSplits = 4;                 // a layer's columns are split over 1, 2, 4 or 8 CTAs
 
 struct LArg {
   const uint8_t* codes;
@@ -275,48 +275,48 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
   auto kernel = w4_gemv_kernel<G, XB, kCap>;
   cudaError_t err = allow_smem(kernel, R::kBytes, &done);
   if (err != cudaSuccess) return err;
-  auto stages = [&](int i, int split) {  // of one CTA of layer i
-    return (Ls[i].cols / kCols + split * kWarps) / (split * kWarps);
-  };
-  auto tiles = [&](int i) { return (Ls[i].rows + kRows - 1) / kRows; };
-  // How far to split the columns.  Halving the longest slice helps while CTAs are few or long ones end last, and
-  // costs each CTA its start and join (kStart stages' time): the least of (work per slot) + (longest slice).
-  constexpr int kStart = 20;
-  int split[kCap], best = 0;
-  double best_cost = 0.0;
-  int64_t longest = 0;
-  for (int i = 0; i < count; ++i) longest = stages(i, 1) > longest ? stages(i, 1) : longest;
+  // Stages of a warp of layer i where its columns are split over 2^k CTAs, and its row tiles.
+  int64_t stages[kCap][kSplits], tiles[kCap], longest = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t units = (Ls[i].cols + kCols - 1) / kCols;
+    for (int k = 0; k < kSplits; ++k) stages[i][k] = (units + (kWarps << k) - 1) / (kWarps << k);
+    tiles[i] = (Ls[i].rows + kRows - 1) / kRows;
+    longest = stages[i][0] > longest ? stages[i][0] : longest;
+  }
   auto split_for = [&](int i, int64_t len) {
-    int sp = 1;
-    while (sp < kMaxCluster && stages(i, sp) > len) sp *= 2;
-    return sp;
+    int k = 0;
+    while (k + 1 < kSplits && stages[i][k] > len) ++k;
+    return k;
   };
-  for (int q = 1; q <= kMaxCluster; q *= 2) {
-    const int64_t len = (longest + q - 1) / q;
-    double work = 0.0;
-    int64_t top = 0;
+  // How far to split the columns.  Halving the longest slice helps while CTAs are few or long ones end last, and
+  // costs each CTA its start and join (kStart stages' time): the least of (work per slot) + (longest slice) / 2.
+  constexpr int kStart = 6;
+  int best = 0;
+  int64_t best_cost = 0;
+  for (int q = 0; q < kSplits; ++q) {
+    const int64_t len = (longest + (1 << q) - 1) >> q;
+    int64_t work = 0, top = 0;
     for (int i = 0; i < count; ++i) {
-      const int sp = split_for(i, len);
-      const int64_t st = stages(i, sp);
-      work += (double)(tiles(i) * sp) * (double)(st + kStart);
-      top = st > top ? st : top;
+      const int k = split_for(i, len);
+      work += (tiles[i] << k) * (stages[i][k] + kStart);
+      top = stages[i][k] > top ? stages[i][k] : top;
     }
-    const double cost = work / (148.0 * R::kCtas) + 0.5 * (double)(top + kStart);
-    if (best == 0 || cost < best_cost) {
+    const int64_t cost = 2 * work / (148 * R::kCtas) + top;
+    if (q == 0 || cost < best_cost) {
       best = q;
       best_cost = cost;
     }
   }
-  int cluster = 1;
+  int split[kCap], cluster = 1;
   for (int i = 0; i < count; ++i) {
-    split[i] = split_for(i, (longest + best - 1) / best);
-    cluster = split[i] > cluster ? split[i] : cluster;
+    split[i] = split_for(i, (longest + (1 << best) - 1) >> best);
+    cluster = (1 << split[i]) > cluster ? 1 << split[i] : cluster;
   }
   // the longest slices first, so that the last CTAs to start are short ones
   int order[kCap];
   for (int i = 0; i < count; ++i) {
     int j = i;
-    for (; j > 0 && stages(order[j - 1], split[order[j - 1]]) < stages(i, split[i]); --j) order[j] = order[j - 1];
+    for (; j > 0 && stages[order[j - 1]][split[order[j - 1]]] < stages[i][split[i]]; --j) order[j] = order[j - 1];
     order[j] = i;
   }
   LParams<kCap> p;
@@ -338,8 +338,8 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
     l.cols = (int32_t)a.cols;
     l.x_split = a.x_im ? a.cols / 2 : a.cols;
     l.y_split = a.y_im ? a.rows / 2 : a.rows;
-    l.split = split[order[i]];
-    l.tiles = (int32_t)tiles(order[i]);
+    l.split = 1 << split[order[i]];
+    l.tiles = (int32_t)tiles[order[i]];
     l.cluster_begin = (int32_t)clusters;
     const int64_t each = cluster / l.split;  // row tiles of a cluster
     clusters += (l.tiles + each - 1) / each;
