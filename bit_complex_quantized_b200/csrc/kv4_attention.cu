@@ -3,24 +3,36 @@
 // keys j <= the token's position, o's planes summed separately.
 //
 // One pass over the cache with the running maximum and sum of the softmax.  A warp takes 32 keys at a
-// time (two records): keys are the rows of the matrix instruction's A operand, queries the columns of B.
-//   q     float32, times scale log2 e, split into two bf16 terms (high, low: 2^-16 relative) that
-//         are two neighbouring columns, so that the scores keep float32's order of accuracy
-//   K     codes minus 8, exact; s and m of a key's plane enter per score in float32:
-//         score = sum_planes s (codes . q) + (m + 8 s) sum(q)
-//   P     p s per key and plane, split the same way, transposed in registers (movmatrix) from the
-//         score layout into the B operand; o = sum_j (p s)_j codes_j + sum_j p_j (m + 8 s)_j
-// A product of a column pair is added up within one lane.
+// time (two records, copied asynchronously into a ring of its own): keys are the rows of the matrix
+// instruction's A operand, queries the columns of B, all in fp16 with float32 sums.
+//   codes  four bits of a word under a mask are already a number: n 2^-24 in bits 0-3 of an fp16, 16 n 2^-24 in
+//          bits 4-7 (subnormal and first normal numbers share one spacing), so an operand register
+//          costs one AND; the 16 is undone in q's columns (keys) or in the output's rows (values)
+//   q      float32, scaled by a power of two per row to below 2^15 and split into two fp16 terms
+//          (2^-22 of the row's largest entry) that are two neighbouring columns
+//   K      score = scale sum_planes s (codes . q) + m sum(q), s and m of a key's plane, in float32
+//   P      p s 2^15 / cap as one fp16 term (2^-12 relative, 2^-40 of the cap absolute), cap a power of two
+//          above every s seen (raised, with the sums rescaled, when a larger one comes), transposed in
+//          registers (movmatrix) from the score layout into the B operand;
+//          o = sum_j (p s)_j codes_j + sum_j p_j m_j, the second sum in float32
+// A query row's score is the sum of its two columns, within one lane; its weights are one column.
+//
+// Work split: (key/value head and tile of 8 query rows, sequence) x splits of the keys; the four warps of a
+// CTA and the CTAs of a cluster (up to 8 splits) join their parts in shared memory, in a fixed
+// order; more splits than a cluster holds are joined by a second, small kernel.
 #include "ifq_internal.h"
 #include "kv4_common.cuh"
+
+#include <cuda_fp16.h>
 
 namespace ifq {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 32;                  // keys of a warp's step
-constexpr int kBlockKeys = kWarps * kStep;
+constexpr int kUnit = 32;                  // keys of a warp's step: two records
+constexpr int kStages = 2;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 64;
 
 struct AttnParams {
@@ -30,9 +42,9 @@ struct AttnParams {
   int64_t ldq, ldo;
   float scale2;      // scale log2 e
   int32_t shared;    // query heads of a key/value head
-  int32_t splits, qtiles;
-  float* ws_o;       // [B][kv_heads][qtiles QR][splits][D]
-  float2* ws_ml;     // [B][kv_heads][qtiles QR][splits]: maximum (log2), sum
+  int32_t splits, cluster, qtiles;
+  float* ws_o;       // [B][kv_heads][qtiles QR][splits / cluster][D]
+  float2* ws_ml;     // [B][kv_heads][qtiles QR][splits / cluster]: maximum (log2), sum
   uint32_t* status;
 };
 
@@ -45,207 +57,385 @@ IFQ_DEVINL float ex2(float x) {
 // 8 x 8 transpose of 16-bit elements over a warp.
 IFQ_DEVINL uint32_t movmatrix(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-// v as two bf16 terms, the larger in the low half.
-IFQ_DEVINL uint32_t split_bf16(float v) {
-  const float hi = __bfloat162float(__float2bfloat16_rn(v));
-  return pack_bf16(hi, v - hi);
+IFQ_DEVINL uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
-// Keys of a split of a sequence of len keys: whole blocks, shared evenly.
-IFQ_DEVINL int32_t split_keys(int32_t len, int32_t splits) {
-  const int32_t blocks = (len + kBlockKeys - 1) / kBlockKeys;
-  return (blocks + splits - 1) / splits * kBlockKeys;
+IFQ_DEVINL void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+IFQ_DEVINL void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// The four operand registers of a word: codes times 2^-24 (first and third) and 2^-20 (second and fourth).
+IFQ_DEVINL void codes_f16(uint32_t w, uint32_t (&a)[4]) {
+  const uint32_t v = w >> 8;
+  a[0] = w & 0x000F000Fu;
+  a[1] = w & 0x00F000F0u;
+  a[2] = v & 0x000F000Fu;
+  a[3] = v & 0x00F000F0u;
+}
+
+// 2^e as a float, for -126 <= e <= 127.
+IFQ_DEVINL float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// Units of a warp of the sequence's key range; the call's warps take them in turn.
+__host__ __device__ inline int32_t warp_units(int32_t len, int32_t splits) {
+  const int32_t units = (len + kUnit - 1) / kUnit, parts = splits * kWarps;
+  return (units + parts - 1) / parts;
+}
+// Clusters of a sequence that hold keys (at least one, which writes the zeros of an empty sequence).
+IFQ_DEVINL int32_t used_groups(int32_t len, int32_t splits, int32_t cluster) {
+  const int32_t per = warp_units(len, splits) * kWarps * cluster * kUnit;
+  return len > 0 ? (len + per - 1) / per : 1;
+}
+
+IFQ_DEVINL void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+IFQ_DEVINL float2 ld_cluster2(const void* smem, uint32_t rank) {
+  uint32_t a;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(smem)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
 }
 
 template <int DIM, int NT>
+struct Layout {
+  static constexpr int D = 2 * DIM, CH = D / 32, QR = 4 * NT;
+  static constexpr int kRecord = 16 * D + 256;
+  static constexpr int kStage = 2 * kRecord;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kQ = NT * CH * 512;                     // B operands of q
+  static constexpr int kBytes = kRing + kQ;
+  static constexpr int kSums = kWarps * QR * D * 4;            // in the ring's memory
+  static_assert(kSums <= kRing, "the sums reuse the ring");
+};
+
+template <int DIM, int NT>
 __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int D = 2 * DIM, CH = D / 32, CP = DIM / 32, QR = 4 * NT, T4 = D / 64;
-  __shared__ uint4 qs[NT][CH][32];          // B operands of q
-  __shared__ float qsum[QR][2];             // sum of a query's plane
-  __shared__ float os[kWarps][QR][D];
+  using Y = Layout<DIM, NT>;
+  constexpr int D = Y::D, CH = Y::CH, CP = DIM / 32, QR = Y::QR, T4 = D / 64;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float qsum[QR][2];             // 2^-24 sum of a scaled query's plane
+  __shared__ int qexp[QR];                  // exponent of a query row's largest entry
   __shared__ float2 mls[kWarps][QR];
+  __shared__ float2 ml_cta[QR];
+  uint4* qs = reinterpret_cast<uint4*>(smem + Y::kRing);
   const Kv4Arg& c = p.c;
   const int b = blockIdx.z, kvh = blockIdx.y / p.qtiles, qt = blockIdx.y % p.qtiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Kv4Seq sq = kv4_seq(c, b);
   if (!sq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   const int nrows = sq.n_new * p.shared - qt * QR;  // query rows of this tile
-  if (nrows <= 0) return;
-  const int32_t per = split_keys(sq.len, p.splits);
-  const int32_t k_begin = (int32_t)blockIdx.x * per;
-  const int32_t k_end = min(sq.len, k_begin + per);
-  if (blockIdx.x > 0 && k_begin >= k_end) return;
+  const int group = (int)blockIdx.x / p.cluster, rank = (int)blockIdx.x % p.cluster;
+  if (nrows <= 0 || group >= used_groups(sq.len, p.splits, p.cluster)) return;  // the whole cluster
 
-  // q: thread (nt, ch, lane) of the operand order
-  for (int i = threadIdx.x; i < NT * CH * 32; i += kThreads) {
+  // this warp's tiles (records) of the sequence, contiguous
+  const int32_t per = warp_units(sq.len, p.splits);
+  const int32_t tiles = (sq.len + 15) >> 4;
+  const int32_t t_begin = min(tiles, ((int32_t)blockIdx.x * kWarps + warp) * per * 2);
+  const int32_t t_end = min(tiles, t_begin + per * 2);
+
+  // Record numbers, 32 tiles at a time (lane l: tile base + l), the next 32 on their way.
+  auto fetch = [&](int32_t base) -> uint32_t {
+    const int32_t tl = base + lane;
+    if (tl >= t_end) return 0xFFFFFFFFu;
+    const int32_t pc = (int32_t)((uint32_t)tl / (uint32_t)c.page_tiles), in = tl - pc * c.page_tiles;
+    const int32_t page = __ldg(c.page_table + (int64_t)b * c.table_cols + pc);
+    if (page < 0 || page >= c.pages) {
+      set_status(p.status, IFQ_DEV_RANGE);
+      return 0xFFFFFFFFu;
+    }
+    return ((uint32_t)page * c.kv_heads + kvh) * c.page_tiles + in;
+  };
+  uint32_t rec_now = fetch(t_begin), rec_next = fetch(t_begin + 32);
+  const uint32_t ring = smem_u32(smem) + warp * kStages * Y::kStage + lane * 16;
+  uint32_t ok = 0;          // bit 2 slot + i: record i of the slot's stage is there
+  int32_t tl = t_begin;     // first tile of the next load
+  auto load = [&](int slot) {
+    if (tl < t_end) {
+      ok &= ~(3u << (2 * slot));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t r = __shfl_sync(0xffffffffu, rec_now, (tl - t_begin + i) & 31);
+        if (r != 0xFFFFFFFFu) {
+          ok |= 1u << (2 * slot + i);
+          const uint8_t* src = c.records + (uint64_t)r * Y::kRecord + lane * 16;
+          const uint32_t dst = ring + slot * Y::kStage + i * Y::kRecord;
+#pragma unroll
+          for (int v = 0; v < Y::kRecord / 512; ++v) cp_async16(dst + v * 512, src + v * 512);
+          if (lane < Y::kRecord % 512 / 16) cp_async16(dst + Y::kRecord / 512 * 512, src + Y::kRecord / 512 * 512);
+        }
+      }
+      tl += 2;
+      if (((tl - t_begin) & 31) == 0) {
+        rec_now = rec_next;
+        rec_next = fetch(tl + 32);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < kStages - 1; ++st) load(st);
+
+  // q: a row's largest exponent and plane sums (a warp per row), then the operands
+  auto q_row = [&](int row, int d) -> const float* {
+    const int rr = qt * QR + row, tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
+    return p.q[d / DIM] + (sq.row0 + tok) * p.ldq + head * DIM + d % DIM;
+  };
+  for (int row = warp; row < QR; row += kWarps) {
+    float mx = 0.0f, sum[2] = {};
+    bool bad = false;
+    if (row < nrows)
+#pragma unroll
+      for (int d = lane * 2; d < D; d += 64) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(q_row(row, d)));
+        mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+        bad |= !(fabsf(v.x) <= 3.402823466e38f) || !(fabsf(v.y) <= 3.402823466e38f);
+      }
+    if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // mx < 2^(e + 1); a zero or subnormal row keeps the smallest exponent, an infinite one becomes NaN below
+    const int e = max((__float_as_int(mx) >> 23) - 127, -100);
+    const float f = pow2(min(14 - e, 127)) ;
+    if (row < nrows)
+#pragma unroll
+      for (int d = lane * 2; d < D; d += 64) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(q_row(row, d)));
+        sum[d / DIM] += f * v.x + f * v.y;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+    }
+    if (lane == 0) {
+      qexp[row] = e;
+      qsum[row][0] = sum[0] * 0x1p-24f;
+      qsum[row][1] = sum[1] * 0x1p-24f;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * CH * 32; i += kThreads) {  // thread (nt, ch, lane) of the operand order
     const int ln = i & 31, ch = (i >> 5) % CH, nt = (i >> 5) / CH;
     const int row = nt * 4 + (ln >> 3), part = (ln >> 2) & 1;
     uint32_t w[4] = {};
     if (row < nrows) {
-      const int rr = qt * QR + row, tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
-      const int d = ch * 32 + (ln & 3) * 8;
-      const float* src = p.q[d / DIM] + (sq.row0 + tok) * p.ldq + head * DIM + d % DIM;
+      const float4* src = reinterpret_cast<const float4*>(q_row(row, ch * 32 + (ln & 3) * 8));
+      const float f = pow2(min(14 - qexp[row], 127));
+      const float4 a = __ldg(src), bq = __ldg(src + 1);
+      float v[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(src) + j);
-        const uint32_t a = split_bf16(v.x * p.scale2), bq = split_bf16(v.y * p.scale2);
-        w[j] = part ? (a >> 16) | (bq & 0xFFFF0000u) : (a & 0xFFFFu) | (bq << 16);
-        if (!(fabsf(v.x) <= 3.402823466e38f) || !(fabsf(v.y) <= 3.402823466e38f))
-          set_status(p.status, IFQ_DEV_NONFINITE);
+      for (int j = 0; j < 8; ++j) {
+        v[j] *= (j & 2) ? f * 0x1p-4f : f;  // entries 2, 3, 6, 7 meet codes times 16
+        if (part) v[j] -= __half2float(__float2half_rn(v[j]));
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_f16(v[2 * j], v[2 * j + 1]);
     }
-    qs[nt][ch][ln] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < QR * 2; i += kThreads) {
-    const int row = i >> 1, pl = i & 1;
-    float sum = 0.0f;
-    for (int ch = pl * CP; ch < (pl + 1) * CP; ++ch)
-      for (int l = 0; l < 8; ++l) {
-        const uint4 v = qs[row >> 2][ch][(row & 3) * 8 + l];
-        sum += (bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y)) + (bf16_lo(v.z) + bf16_hi(v.z)) +
-               (bf16_lo(v.w) + bf16_hi(v.w));
-      }
-    qsum[row][pl] = sum;
+    qs[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncthreads();
 
-  float qs2[NT][2];
+  float qs2[NT][2], cs[NT];
   int32_t visible[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = nt * 4 + t;
     qs2[nt][0] = qsum[row][0];
     qs2[nt][1] = qsum[row][1];
+    cs[nt] = p.scale2 * pow2(min(qexp[row], 127)) * 1024.0f;  // undoes the 2^-24 of the codes and the row's 2^(14 - e)
     visible[nt] = row < nrows ? sq.len - sq.n_new + (qt * QR + row) / p.shared + 1 : 0;
   }
+  // keys below this are seen by every row of the tile (rows past the last count as seeing all)
+  const int32_t vis_all = sq.len - sq.n_new + qt * QR / p.shared + 1;
 
-  float acc[CH][2][NT][4];
+  float acc[CH][2][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[i][j][nt][0] = acc[i][j][nt][1] = acc[i][j][nt][2] = acc[i][j][nt][3] = 0.0f;
+    for (int j = 0; j < 2; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
   float m_run[NT], l_run[NT], pm[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m_run[nt] = -INFINITY;
     l_run[nt] = pm[nt][0] = pm[nt][1] = 0.0f;
   }
+  float cap[2] = {0.0f, 0.0f}, to_w[2] = {0.0f, 0.0f};  // per plane: the cap on s, 2^15 / cap
 
-  for (int32_t key0 = k_begin + warp * kStep; key0 < k_end; key0 += kBlockKeys) {
-    const uint8_t* rec[2];
+  const uint8_t* stage0 = smem + warp * kStages * Y::kStage;
+  auto unit = [&](int slot, int32_t key0) {
+    const uint8_t* base = stage0 + slot * Y::kStage;
+    const bool full = key0 + kUnit <= vis_all && ((ok >> (2 * slot)) & 3u) == 3u;
     float sc[2][NT][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int32_t kt = key0 + 16 * i;
-      rec[i] = kt < k_end ? kv4_record(c, b, kvh, kt >> 4) : nullptr;
-      if (kt < k_end && !rec[i] && lane == 0) set_status(p.status, IFQ_DEV_RANGE);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[i][nt][0] = sc[i][nt][1] = -INFINITY;
-      if (!rec[i]) continue;
-      float s4[2][NT][4] = {};
+      const uint8_t* rec = base + i * Y::kRecord;
+      float s4[2][NT][4];
 #pragma unroll
       for (int v = 0; v < T4; ++v) {
-        const uint4 w4 = ldg_stream(rec[i] + v * 512 + lane * 16);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        const uint4 w4 = *reinterpret_cast<const uint4*>(rec + v * 512 + lane * 16);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int ch = 2 * v + cc, pl = ch / CP;
           uint32_t lo[4], hi[4];
-          q4_expand<kQ4Sub8>(w[2 * cc], lo);
-          q4_expand<kQ4Sub8>(w[2 * cc + 1], hi);
+          codes_f16(cc ? w4.z : w4.x, lo);
+          codes_f16(cc ? w4.w : w4.y, hi);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint4 bq = qs[nt][ch][lane];
-            mma_bf16(s4[pl][nt], lo[0], hi[0], lo[1], hi[1], bq.x, bq.y);
-            mma_bf16(s4[pl][nt], lo[2], hi[2], lo[3], hi[3], bq.z, bq.w);
+            const uint4 bq = qs[(nt * CH + ch) * 32 + lane];
+            if (ch % CP == 0) mma_f16_first(s4[pl][nt], lo[0], hi[0], lo[1], hi[1], bq.x, bq.y);
+            else mma_f16(s4[pl][nt], lo[0], hi[0], lo[1], hi[1], bq.x, bq.y);
+            mma_f16(s4[pl][nt], lo[2], hi[2], lo[3], hi[3], bq.z, bq.w);
           }
         }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint2 par = __ldg(reinterpret_cast<const uint2*>(rec[i] + 16 * D + (g + 8 * h) * 8));
-        const float s0 = bf16_lo(par.x), m0 = fmaf(8.0f, s0, bf16_hi(par.x));
-        const float s1 = bf16_lo(par.y), m1 = fmaf(8.0f, s1, bf16_hi(par.y));
-        const float u0 = s0 * kQ4Unit, u1 = s1 * kQ4Unit;
-        const int32_t key = kt + g + 8 * h;
+        const uint2 par = *reinterpret_cast<const uint2*>(rec + 16 * D + (g + 8 * h) * 8);
+        const float k0 = bf16_lo(par.x), m0 = bf16_hi(par.x), k1 = bf16_lo(par.y), m1 = bf16_hi(par.y);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float a0 = s4[0][nt][2 * h] + s4[0][nt][2 * h + 1], a1 = s4[1][nt][2 * h] + s4[1][nt][2 * h + 1];
-          const float v = fmaf(u0, a0, m0 * qs2[nt][0]) + fmaf(u1, a1, m1 * qs2[nt][1]);
-          sc[i][nt][h] = key < visible[nt] ? v : -INFINITY;
+          sc[i][nt][h] = cs[nt] * fmaf(k0, a0, fmaf(k1, a1, fmaf(m0, qs2[nt][0], m1 * qs2[nt][1])));
         }
       }
     }
-    float mb[NT];
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (key0 + 16 * i + g + 8 * h >= visible[nt] || !((ok >> (2 * slot + i)) & 1u)) sc[i][nt][h] = -INFINITY;
+    }
+    float mn[NT];
+    bool grew = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float mx = fmaxf(fmaxf(sc[0][nt][0], sc[0][nt][1]), fmaxf(sc[1][nt][0], sc[1][nt][1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      const float mn = fmaxf(m_run[nt], mx);
-      mb[nt] = mn == -INFINITY ? 0.0f : mn;
-      const float al = ex2(m_run[nt] - mb[nt]);
-      m_run[nt] = mn;
-      l_run[nt] *= al;
-      pm[nt][0] *= al;
-      pm[nt][1] *= al;
+      mn[nt] = fmaxf(m_run[nt], mx);
+      grew |= mn[nt] > m_run[nt];
+    }
+    // the values' scales of this lane's keys: {key, plane}; 0 for keys that nobody sees
+    float vs[2][2][2], vm[2][2][2];
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 par = *reinterpret_cast<const uint2*>(base + i * Y::kRecord + 16 * D + 128 + (g + 8 * h) * 8);
+        const bool in = full || (key0 + 16 * i + g + 8 * h < sq.len && ((ok >> (2 * slot + i)) & 1u));
+        vs[i][h][0] = in ? bf16_lo(par.x) : 0.0f;
+        vm[i][h][0] = in ? bf16_hi(par.x) : 0.0f;
+        vs[i][h][1] = in ? bf16_lo(par.y) : 0.0f;
+        vm[i][h][1] = in ? bf16_hi(par.y) : 0.0f;
+      }
+    float top[2];
+#pragma unroll
+    for (int pl = 0; pl < 2; ++pl)
+      top[pl] = fmaxf(fmaxf(vs[0][0][pl], vs[0][1][pl]), fmaxf(vs[1][0][pl], vs[1][1][pl]));
+    grew |= top[0] > cap[0] || top[1] > cap[1];
+    if (__any_sync(0xffffffffu, grew)) {
+      float f[2];  // what a raised cap does to a plane's sums
+#pragma unroll
+      for (int pl = 0; pl < 2; ++pl) {
+        float mx = top[pl];
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        f[pl] = 1.0f;
+        if (mx > cap[pl]) {
+          const int e = min(max((__float_as_int(mx) >> 23) - 127 + 2, -100), 126);  // mx < 2^(e - 1): room to grow
+          f[pl] = cap[pl] * pow2(-e);
+          cap[pl] = pow2(e);
+          to_w[pl] = pow2(15 - e);
+        }
+      }
+      float al[2] = {1.0f, 1.0f};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        al[nt] = mn[nt] == -INFINITY ? 1.0f : ex2(m_run[nt] - mn[nt]);
+        m_run[nt] = mn[nt];
+        l_run[nt] *= al[nt];
+        pm[nt][0] *= al[nt];
+        pm[nt][1] *= al[nt];
+      }
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][nt][e] *= al;
+          for (int e = 0; e < 4; ++e) acc[ch][j][e] *= al[e & 1] * f[ch / CP];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (!rec[i]) continue;
-      uint32_t pb[2][NT][2];  // B operands of p s: plane, n tile, keys 0-7 / 8-15
+      uint32_t pb[2][2];  // B operands of p s: plane, keys 0-7 / 8-15
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint2 par = __ldg(reinterpret_cast<const uint2*>(rec[i] + 16 * D + 128 + (g + 8 * h) * 8));
-        const float s0 = bf16_lo(par.x), m0 = fmaf(8.0f, s0, bf16_hi(par.x));
-        const float s1 = bf16_lo(par.y), m1 = fmaf(8.0f, s1, bf16_hi(par.y));
+        const float w0 = vs[i][h][0] * to_w[0], w1 = vs[i][h][1] * to_w[1];
+        float pr[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float pr = ex2(sc[i][nt][h] - mb[nt]);
-          l_run[nt] += pr;
-          // rows behind the last key hold whatever the page held: their weight is zero, not their product
-          const bool on = sc[i][nt][h] != -INFINITY;
-          pm[nt][0] += on ? pr * m0 : 0.0f;
-          pm[nt][1] += on ? pr * m1 : 0.0f;
-          pb[0][nt][h] = movmatrix(on ? split_bf16(pr * s0) : 0u);
-          pb[1][nt][h] = movmatrix(on ? split_bf16(pr * s1) : 0u);
+          pr[nt] = ex2(sc[i][nt][h] - (m_run[nt] == -INFINITY ? 0.0f : m_run[nt]));
+          l_run[nt] += pr[nt];
+          pm[nt][0] = fmaf(pr[nt], vm[i][h][0], pm[nt][0]);
+          pm[nt][1] = fmaf(pr[nt], vm[i][h][1], pm[nt][1]);
         }
+        pb[0][h] = movmatrix(pack_f16(pr[0] * w0, pr[1] * w0));
+        pb[1][h] = movmatrix(pack_f16(pr[0] * w1, pr[1] * w1));
       }
 #pragma unroll
       for (int v = 0; v < T4; ++v) {
-        const uint4 w4 = ldg_stream(rec[i] + 8 * D + v * 512 + lane * 16);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        const uint4 w4 = *reinterpret_cast<const uint4*>(base + i * Y::kRecord + 8 * D + v * 512 + lane * 16);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int ch = 2 * v + cc, pl = ch / CP;
           uint32_t lo[4], hi[4];
-          q4_expand<kQ4Sub8>(w[2 * cc], lo);
-          q4_expand<kQ4Sub8>(w[2 * cc + 1], hi);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16(acc[ch][0][nt], lo[0], lo[1], hi[0], hi[1], pb[pl][nt][0], pb[pl][nt][1]);
-            mma_bf16(acc[ch][1][nt], lo[2], lo[3], hi[2], hi[3], pb[pl][nt][0], pb[pl][nt][1]);
-          }
+          codes_f16(cc ? w4.z : w4.x, lo);
+          codes_f16(cc ? w4.w : w4.y, hi);
+          mma_f16(acc[ch][0], lo[0], lo[1], hi[0], hi[1], pb[pl][0], pb[pl][1]);
+          mma_f16(acc[ch][1], lo[2], lo[3], hi[2], hi[3], pb[pl][0], pb[pl][1]);
         }
       }
     }
-  }
+  };
 
-  // the warps' parts, then their sum
+  for (int32_t tt = t_begin; tt < t_end;) {
+#pragma unroll
+    for (int slot = 0; slot < kStages; ++slot, tt += 2) {
+      if (tt >= t_end) break;
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // every lane's copies of the stage are in, and the previous stage has been read
+      load((slot + kStages - 1) % kStages);
+      unit(slot, tt * 16);
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // the warps' parts, then their sum, then the cluster's
+  float* os = reinterpret_cast<float*>(smem);  // [warp][row][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -258,16 +448,32 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
     if (g == 0) mls[warp][row] = make_float2(m_run[nt], l_run[nt]);
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      const float pmv = pm[nt][ch / CP];
+      const float pmv = pm[nt][ch / CP], k = cap[ch / CP];
       float4 v;
-      v.x = fmaf(kQ4Unit, acc[ch][0][nt][0] + acc[ch][0][nt][1], pmv);
-      v.y = fmaf(kQ4Unit, acc[ch][0][nt][2] + acc[ch][0][nt][3], pmv);
-      v.z = fmaf(kQ4Unit, acc[ch][1][nt][0] + acc[ch][1][nt][1], pmv);
-      v.w = fmaf(kQ4Unit, acc[ch][1][nt][2] + acc[ch][1][nt][3], pmv);
-      *reinterpret_cast<float4*>(&os[warp][row][ch * 32 + 4 * g]) = v;
+      v.x = fmaf(acc[ch][0][nt] * 0x1p9f, k, pmv);
+      v.y = fmaf(acc[ch][0][2 + nt] * 0x1p5f, k, pmv);
+      v.z = fmaf(acc[ch][1][nt] * 0x1p9f, k, pmv);
+      v.w = fmaf(acc[ch][1][2 + nt] * 0x1p5f, k, pmv);
+      *reinterpret_cast<float4*>(&os[(warp * QR + row) * D + ch * 32 + 4 * g]) = v;
     }
   }
   __syncthreads();
+  const bool joined = p.cluster > 1;
+  const int64_t row_base = ((int64_t)b * c.kv_heads + kvh) * p.qtiles * QR + qt * QR;
+  const int groups = p.splits / p.cluster;
+  // o and (M, l) of a row's pair of entries: to the output, or as a partial result
+  auto store = [&](int row, int d, float M, float l, float o0, float o1) {
+    if (groups == 1) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int rr = qt * QR + row, tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
+      *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (sq.row0 + tok) * p.ldo + head * DIM + d % DIM) =
+          pack_bf16(o0 * inv, o1 * inv);
+    } else {
+      const int64_t at = (row_base + row) * groups + group;
+      *reinterpret_cast<float2*>(p.ws_o + at * D + d) = make_float2(o0, o1);
+      if (d == 0) p.ws_ml[at] = make_float2(M, l);
+    }
+  };
   for (int i = threadIdx.x; i < QR * (D / 2); i += kThreads) {
     const int row = i / (D / 2), d = (i % (D / 2)) * 2;
     if (row >= nrows) break;
@@ -279,25 +485,41 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = ex2(mls[w][row].x - ms);
+      const float2 v = *reinterpret_cast<const float2*>(&os[(w * QR + row) * D + d]);
       l += f * mls[w][row].y;
-      o0 += f * os[w][row][d];
-      o1 += f * os[w][row][d + 1];
+      o0 += f * v.x;
+      o1 += f * v.y;
     }
-    const int rr = qt * QR + row;
-    if (p.splits == 1) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
-      *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (sq.row0 + tok) * p.ldo + head * DIM + d % DIM) =
-          pack_bf16(o0 * inv, o1 * inv);
+    if (joined) {
+      *reinterpret_cast<float2*>(&os[row * D + d]) = make_float2(o0, o1);  // over warp 0's part, read by this thread alone
+      if (d == 0) ml_cta[row] = make_float2(M, l);
     } else {
-      const int64_t at = ((((int64_t)b * c.kv_heads + kvh) * p.qtiles * QR) + rr) * p.splits + blockIdx.x;
-      *reinterpret_cast<float2*>(p.ws_o + at * D + d) = make_float2(o0, o1);
-      if (d == 0) p.ws_ml[at] = make_float2(M, l);
+      store(row, d, M, l, o0, o1);
     }
   }
+  if (!joined) return;
+  cluster_sync();
+  const int pairs = QR * (D / 2) / p.cluster;
+  for (int i = rank * pairs + threadIdx.x; i < (rank + 1) * pairs; i += kThreads) {
+    const int row = i / (D / 2), d = (i % (D / 2)) * 2;
+    if (row >= nrows) break;
+    float M = -INFINITY;
+    for (int k = 0; k < p.cluster; ++k) M = fmaxf(M, ld_cluster2(&ml_cta[row], k).x);
+    const float ms = M == -INFINITY ? 0.0f : M;
+    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    for (int k = 0; k < p.cluster; ++k) {
+      const float2 ml = ld_cluster2(&ml_cta[row], k), v = ld_cluster2(&os[row * D + d], k);
+      const float f = ex2(ml.x - ms);
+      l += f * ml.y;
+      o0 += f * v.x;
+      o1 += f * v.y;
+    }
+    store(row, d, M, l, o0, o1);
+  }
+  cluster_sync();  // no CTA leaves while its sums are being read
 }
 
-// The splits of a query row, added in their order.  One warp per query row.
+// The groups of splits of a query row, added in their order.  One warp per query row.
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_constant__ AttnParams p, int qr) {
   constexpr int D = 2 * DIM;
@@ -306,9 +528,8 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_consta
   const int rr = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const Kv4Seq sq = kv4_seq(c, b);
   if (rr >= sq.n_new * p.shared) return;
-  const int32_t per = split_keys(sq.len, p.splits);
-  const int used = sq.len > 0 ? (sq.len + per - 1) / per : 1;
-  const int64_t at = (((int64_t)b * c.kv_heads + kvh) * p.qtiles * qr + rr) * p.splits;
+  const int used = used_groups(sq.len, p.splits, p.cluster);
+  const int64_t at = (((int64_t)b * c.kv_heads + kvh) * p.qtiles * qr + rr) * (p.splits / p.cluster);
   float M = -INFINITY;
   for (int s = 0; s < used; ++s) M = fmaxf(M, p.ws_ml[at + s].x);
   const float ms = M == -INFINITY ? 0.0f : M;
@@ -336,35 +557,65 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_consta
 }
 
 struct Plan {
-  int nt, qtiles, splits;
+  int nt, qtiles, splits, cluster;
 };
 
-// Two n tiles (8 query rows) where there are more than 4 query rows; as many splits as fill the GPU.
+// Two n tiles (8 query rows) where there are more than 4 query rows.  Splits, a power of two: until the CTAs
+// fill the GPU or a warp would have less than one step of the longest sequence that the table can hold.
 Plan plan(const ifq_kv4_cache& c, int shared) {
   Plan r;
   const int64_t rows = (int64_t)c.n_new * shared;
   r.nt = rows > 4 ? 2 : 1;
   r.qtiles = (int)((rows + 4 * r.nt - 1) / (4 * r.nt));
   const int64_t ctas = (int64_t)c.B * c.kv_heads * r.qtiles;
-  const int64_t blocks = (c.table_cols * c.page_tokens + kBlockKeys - 1) / kBlockKeys;
-  int64_t s = (148 * 4 + ctas - 1) / ctas;
-  if (s > blocks) s = blocks;
-  if (s > kMaxSplits) s = kMaxSplits;
-  r.splits = s < 1 ? 1 : (int)s;
+  const int64_t keys = c.table_cols * c.page_tokens;
+  r.splits = 1;
+  while (r.splits < kMaxSplits && ctas * r.splits < 148 * 4 && (int64_t)r.splits * kWarps * kUnit < keys) r.splits *= 2;
+  r.cluster = r.splits < kMaxCluster ? r.splits : kMaxCluster;
   return r;
 }
 
 int64_t partials(const ifq_kv4_cache& c, const Plan& r) {
-  return (int64_t)c.B * c.kv_heads * r.qtiles * 4 * r.nt * r.splits;
+  return (int64_t)c.B * c.kv_heads * r.qtiles * 4 * r.nt * (r.splits / r.cluster);
+}
+
+// The kernel's shared memory above 48 KB has to be allowed once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, uint64_t* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (__atomic_load_n(done, __ATOMIC_ACQUIRE) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) __atomic_fetch_or(done, (uint64_t)1 << dev, __ATOMIC_RELEASE);
+  return e;
+}
+
+template <int DIM, int NT>
+cudaError_t launch_nt(const AttnParams& p, cudaStream_t s) {
+  static uint64_t done = 0;
+  auto kernel = kv4_attn_kernel<DIM, NT>;
+  constexpr int bytes = Layout<DIM, NT>::kBytes;
+  cudaError_t e = allow_smem(kernel, bytes, &done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.splits, (unsigned)(p.c.kv_heads * p.qtiles), (unsigned)p.c.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int DIM>
 cudaError_t launch(const AttnParams& p, const Plan& r, cudaStream_t s) {
-  const dim3 grid((unsigned)r.splits, (unsigned)(p.c.kv_heads * r.qtiles), (unsigned)p.c.B);
-  if (r.nt == 1) kv4_attn_kernel<DIM, 1><<<grid, kThreads, 0, s>>>(p);
-  else kv4_attn_kernel<DIM, 2><<<grid, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || r.splits == 1) return e;
+  cudaError_t e = r.nt == 1 ? launch_nt<DIM, 1>(p, s) : launch_nt<DIM, 2>(p, s);
+  if (e != cudaSuccess || r.splits == r.cluster) return e;
   const dim3 mg((unsigned)((p.c.n_new * p.shared + kWarps - 1) / kWarps), (unsigned)p.c.kv_heads, (unsigned)p.c.B);
   kv4_merge_kernel<DIM><<<mg, kThreads, 0, s>>>(p, 4 * r.nt);
   return cudaGetLastError();
@@ -374,7 +625,7 @@ cudaError_t launch(const AttnParams& p, const Plan& r, cudaStream_t s) {
 
 size_t kv4_attention_workspace_bytes(const ifq_kv4_cache& c, int shared) {
   const Plan r = plan(c, shared);
-  if (r.splits == 1) return 0;
+  if (r.splits == r.cluster) return 0;
   return (size_t)partials(c, r) * (2 * c.dim + 2) * 4;
 }
 
@@ -393,6 +644,7 @@ cudaError_t launch_kv4_attention(const ifq_kv4_cache& c, int shared, const float
   p.scale2 = scale * 1.4426950408889634f;
   p.shared = shared;
   p.splits = r.splits;
+  p.cluster = r.cluster;
   p.qtiles = r.qtiles;
   p.ws_o = static_cast<float*>(ws);
   p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + partials(c, r) * 2 * c.dim);

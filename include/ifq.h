@@ -542,10 +542,11 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *                    sequence sees positions 0 .. len - n + i (itself included,
  *                    so append first).  o_re, o_im [rows][q_heads dim] bf16, rows
  *                    ldo apart.  score = scale Re(q^T conj(k)).  n_new <=
- *                    IFQ_KV4_MAX_NEW.  A row that sees no key is 0.  q enters as two bf16
- *                    terms (2^-16 relative), the weights of v likewise; sums and the
- *                    softmax's maximum and sum are float32; partial results are
- *                    joined in a fixed order (bit-reproducible).  A NaN or Inf in q
+ *                    IFQ_KV4_MAX_NEW.  A row that sees no key is 0.  q enters as two fp16
+ *                    terms (2^-22 of the row's largest entry), the weights times a value's scale as one
+ *                    (2^-11 relative); sums and the softmax's maximum and sum are float32, and
+ *                    stay finite for stored values up to 2^100; partial results are joined in a
+ *                    fixed order (bit-reproducible).  A NaN or Inf in q
  *                    sets IFQ_DEV_NONFINITE and makes that row NaN.
  *   workspace        device scratch of ifq_kv4_attention_workspace_bytes() bytes,
  *                    16-byte aligned, no initial contents needed; calls that share it

@@ -126,7 +126,7 @@ def kv4_get(records, dim):
 
 def kv4_attention(q, k, v, first, scale):
     """q float64 [rows][D]; k, v: (n, s, m) of a head's tokens; row i sees keys 0 .. first + i.  Returns (o, bound):
-    bound_id is the first-order error of o from two-term bf16 splits of q and of the weights and from
+    bound is the first-order error of o from a two-term fp16 split of q, weights held as one fp16 term and
     float32 sums, without o's own rounding."""
     rows, D = q.shape
     T = k[0].shape[0]
@@ -137,13 +137,16 @@ def kv4_attention(q, k, v, first, scale):
         n, s, m = x
         sv, mv = bf16_value(s).astype(np.float64)[..., None], bf16_value(m).astype(np.float64)[..., None]
         val = sv * n + mv
-        return val.reshape(T, D), (np.abs(sv * (n.astype(np.float64) - 8)) + np.abs(mv + 8 * sv)).reshape(T, D)
+        return val.reshape(T, D), (np.abs(sv * n) + np.abs(mv)).reshape(T, D)
 
     kv, ka = parts(k)
     vv, va = parts(v)
     s = scale * (q @ kv.T)
-    # |q - (two bf16 terms)| <= 2^-16 |q|; D products and the parameters' terms are added in float32
-    ds = abs(scale) * (np.abs(q) @ ka.T) * (2.0 ** -16 + (D / 16 + 8) * 2.0 ** -22) + 2.0 ** -22 * np.abs(s)
+    # |q - (two fp16 terms)| <= 2^-22 |q| or, where the second term is subnormal, 2^-36 of the row's largest (the
+    # entries are scaled to below 2^11 or 2^15, subnormal steps are 2^-24); D products and the parameters'
+    # terms are added in float32
+    ds = abs(scale) * ((np.abs(q) @ ka.T) * (2.0 ** -21 + (D / 16 + 8) * 2.0 ** -22) +
+                       2.0 ** -34 * np.abs(q).max(axis=1, keepdims=True) * ka.sum(axis=1)) + 2.0 ** -22 * np.abs(s)
     seen = np.arange(T)[None, :] <= first + np.arange(rows)[:, None]
     o, bound = np.zeros((rows, D)), np.zeros((rows, D))
     for i in range(rows):
@@ -154,7 +157,9 @@ def kv4_attention(q, k, v, first, scale):
         p /= p.sum()
         o[i] = p @ vv[seen[i]]
         # a score off by d moves a weight by the factor exp(2 d) at most (its own and the sum's); the weights'
-        # split 2^-16; float32 sums over the keys, exp2 and the joins of partial results
-        rel = np.expm1(2 * di.max()) + 2.0 ** -16 + (len(si) / 16 + 64) * 2.0 ** -22
-        bound[i] = rel * (p @ va[seen[i]])
+        # rounding to fp16 2^-11, or 2^-25 of 2^15 / cap where subnormal, the cap at most 8 times the largest scale;
+        # float32 sums over the keys, exp2 and the joins of partial results
+        rel = np.expm1(2 * di.max()) + 2.0 ** -11 + (len(si) / 16 + 64) * 2.0 ** -22
+        flush = 2.0 ** -37 * 15 * len(si) * bf16_value(v[1][:len(si)]).max() / np.exp(si - si.max()).sum()
+        bound[i] = rel * (p @ va[seen[i]]) + flush
     return o, bound
