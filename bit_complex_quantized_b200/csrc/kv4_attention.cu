@@ -8,14 +8,15 @@
 //   codes  four bits of a word under a mask are already a number: n 2^-24 in bits 0-3 of an fp16, 16 n 2^-24 in
 //          bits 4-7 (subnormal and first normal numbers share one spacing), so an operand register
 //          costs one AND; the 16 is undone in q's columns (keys) or in the output's rows (values)
-//   q      float32, scaled by a power of two per row to below 2^15 and split into two fp16 terms
-//          (2^-22 of the row's largest entry) that are two neighbouring columns
+//   q      float32 times scale log2 e, scaled by a power of two per row to below 2^15 and split into two fp16
+//          terms (2^-22 of the row's largest entry): two neighbouring columns where a tile has up to 4
+//          query rows, two products into the same sums where it has 8
 //   K      score = scale sum_planes s (codes . q) + m sum(q), s and m of a key's plane, in float32
 //   P      p s 2^15 / cap as one fp16 term (2^-12 relative, 2^-40 of the cap absolute), cap a power of two
 //          above every s seen (raised, with the sums rescaled, when a larger one comes), transposed in
 //          registers (movmatrix) from the score layout into the B operand;
 //          o = sum_j (p s)_j codes_j + sum_j p_j m_j, the second sum in float32
-// A query row's score is the sum of its two columns, within one lane; its weights are one column.
+// A lane holds the scores of one query row (of two, in tiles of 8) for the keys g and g + 8 of a record.
 //
 // Work split: (key/value head and tile of 8 query rows, sequence) x splits of the keys; the four warps of a
 // CTA and the CTAs of a cluster (up to 8 splits) join their parts in shared memory, in a fixed
@@ -121,14 +122,14 @@ struct Layout {
   static constexpr int kRecord = 16 * D + 256;
   static constexpr int kStage = 2 * kRecord;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kQ = NT * CH * 512;                     // B operands of q
+  static constexpr int kQ = NT * CH * 512;                     // B operands of q: [term or 0][chunk][lane]
   static constexpr int kBytes = kRing + kQ;
   static constexpr int kSums = kWarps * QR * D * 4;            // in the ring's memory
   static_assert(kSums <= kRing, "the sums reuse the ring");
 };
 
 template <int DIM, int NT>
-__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
   using Y = Layout<DIM, NT>;
   constexpr int D = Y::D, CH = Y::CH, CP = DIM / 32, QR = Y::QR, T4 = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
 #pragma unroll
       for (int d = lane * 2; d < D; d += 64) {
         const float2 v = __ldg(reinterpret_cast<const float2*>(q_row(row, d)));
-        mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+        mx = fmaxf(mx, fmaxf(fabsf(v.x * p.scale2), fabsf(v.y * p.scale2)));
         bad |= !(fabsf(v.x) <= 3.402823466e38f) || !(fabsf(v.y) <= 3.402823466e38f);
       }
     if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
 #pragma unroll
       for (int d = lane * 2; d < D; d += 64) {
         const float2 v = __ldg(reinterpret_cast<const float2*>(q_row(row, d)));
-        sum[d / DIM] += f * v.x + f * v.y;
+        sum[d / DIM] += f * (v.x * p.scale2) + f * (v.y * p.scale2);
       }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
@@ -233,9 +234,9 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * CH * 32; i += kThreads) {  // thread (nt, ch, lane) of the operand order
-    const int ln = i & 31, ch = (i >> 5) % CH, nt = (i >> 5) / CH;
-    const int row = nt * 4 + (ln >> 3), part = (ln >> 2) & 1;
+  for (int i = threadIdx.x; i < NT * CH * 32; i += kThreads) {
+    const int ln = i & 31, ch = (i >> 5) % CH;
+    const int row = NT == 1 ? ln >> 3 : ln >> 2, part = NT == 1 ? (ln >> 2) & 1 : (i >> 5) / CH;
     uint32_t w[4] = {};
     if (row < nrows) {
       const float4* src = reinterpret_cast<const float4*>(q_row(row, ch * 32 + (ln & 3) * 8));
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
       float v[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] *= (j & 2) ? f * 0x1p-4f : f;  // entries 2, 3, 6, 7 meet codes times 16
+        v[j] = v[j] * p.scale2 * ((j & 2) ? f * 0x1p-4f : f);  // entries 2, 3, 6, 7 meet codes times 16
         if (part) v[j] -= __half2float(__float2half_rn(v[j]));
       }
 #pragma unroll
@@ -254,15 +255,16 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
   }
   __syncthreads();
 
+  // This lane's query rows: t, or 2 t and 2 t + 1.
   float qs2[NT][2], cs[NT];
   int32_t visible[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int row = nt * 4 + t;
-    qs2[nt][0] = qsum[row][0];
-    qs2[nt][1] = qsum[row][1];
-    cs[nt] = p.scale2 * pow2(min(qexp[row], 127)) * 1024.0f;  // undoes the 2^-24 of the codes and the row's 2^(14 - e)
-    visible[nt] = row < nrows ? sq.len - sq.n_new + (qt * QR + row) / p.shared + 1 : 0;
+  for (int j = 0; j < NT; ++j) {
+    const int row = NT * t + j;
+    qs2[j][0] = qsum[row][0];
+    qs2[j][1] = qsum[row][1];
+    cs[j] = pow2(min(qexp[row], 117) + 10);  // undoes the 2^-24 of the codes and the row's 2^(14 - e)
+    visible[j] = row < nrows ? sq.len - sq.n_new + (qt * QR + row) / p.shared + 1 : 0;
   }
   // keys below this are seen by every row of the tile (rows past the last count as seeing all)
   const int32_t vis_all = sq.len - sq.n_new + qt * QR / p.shared + 1;
@@ -284,40 +286,49 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
   auto unit = [&](int slot, int32_t key0) {
     const uint8_t* base = stage0 + slot * Y::kStage;
     const bool full = key0 + kUnit <= vis_all && ((ok >> (2 * slot)) & 3u) == 3u;
+    // scores in units of 1 / cs: {record, row, key g or g + 8}
     float sc[2][NT][2];
+    float s4[2][2][4];  // {record, plane}
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t* rec = base + i * Y::kRecord;
-      float s4[2][NT][4];
+    for (int v = 0; v < T4; ++v) {
+      uint4 w4[2];
 #pragma unroll
-      for (int v = 0; v < T4; ++v) {
-        const uint4 w4 = *reinterpret_cast<const uint4*>(rec + v * 512 + lane * 16);
+      for (int i = 0; i < 2; ++i)
+        w4[i] = *reinterpret_cast<const uint4*>(base + i * Y::kRecord + v * 512 + lane * 16);
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const int ch = 2 * v + cc, pl = ch / CP;
+      for (int cc = 0; cc < 2; ++cc) {
+        const int ch = 2 * v + cc, pl = ch / CP;
+        uint4 bq[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) bq[j] = qs[(j * CH + ch) * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           uint32_t lo[4], hi[4];
-          codes_f16(cc ? w4.z : w4.x, lo);
-          codes_f16(cc ? w4.w : w4.y, hi);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 bq = qs[(nt * CH + ch) * 32 + lane];
-            if (ch % CP == 0) mma_f16_first(s4[pl][nt], lo[0], hi[0], lo[1], hi[1], bq.x, bq.y);
-            else mma_f16(s4[pl][nt], lo[0], hi[0], lo[1], hi[1], bq.x, bq.y);
-            mma_f16(s4[pl][nt], lo[2], hi[2], lo[3], hi[3], bq.z, bq.w);
+          codes_f16(cc ? w4[i].z : w4[i].x, lo);
+          codes_f16(cc ? w4[i].w : w4[i].y, hi);
+          if (ch % CP == 0) mma_f16_first(s4[i][pl], lo[0], hi[0], lo[1], hi[1], bq[0].x, bq[0].y);
+          else mma_f16(s4[i][pl], lo[0], hi[0], lo[1], hi[1], bq[0].x, bq[0].y);
+          mma_f16(s4[i][pl], lo[2], hi[2], lo[3], hi[3], bq[0].z, bq[0].w);
+          if (NT == 2) {
+            mma_f16(s4[i][pl], lo[0], hi[0], lo[1], hi[1], bq[NT - 1].x, bq[NT - 1].y);
+            mma_f16(s4[i][pl], lo[2], hi[2], lo[3], hi[3], bq[NT - 1].z, bq[NT - 1].w);
           }
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint2 par = *reinterpret_cast<const uint2*>(rec + 16 * D + (g + 8 * h) * 8);
+        const uint2 par = *reinterpret_cast<const uint2*>(base + i * Y::kRecord + 16 * D + (g + 8 * h) * 8);
         const float k0 = bf16_lo(par.x), m0 = bf16_hi(par.x), k1 = bf16_lo(par.y), m1 = bf16_hi(par.y);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float a0 = s4[0][nt][2 * h] + s4[0][nt][2 * h + 1], a1 = s4[1][nt][2 * h] + s4[1][nt][2 * h + 1];
-          sc[i][nt][h] = cs[nt] * fmaf(k0, a0, fmaf(k1, a1, fmaf(m0, qs2[nt][0], m1 * qs2[nt][1])));
+        for (int j = 0; j < NT; ++j) {
+          const float a0 = NT == 1 ? s4[i][0][2 * h] + s4[i][0][2 * h + 1] : s4[i][0][2 * h + j];
+          const float a1 = NT == 1 ? s4[i][1][2 * h] + s4[i][1][2 * h + 1] : s4[i][1][2 * h + j];
+          sc[i][j][h] = fmaf(k0, a0, fmaf(k1, a1, fmaf(m0, qs2[j][0], m1 * qs2[j][1])));
         }
       }
-    }
     if (!full) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -335,21 +346,21 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      mn[nt] = fmaxf(m_run[nt], mx);
+      mn[nt] = fmaxf(m_run[nt], mx * cs[nt]);
       grew |= mn[nt] > m_run[nt];
     }
-    // the values' scales of this lane's keys: {key, plane}; 0 for keys that nobody sees
+    // the values' scales and minima of this lane's keys: {record, key, plane}; 0 for keys that do not exist
     float vs[2][2][2], vm[2][2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint2 par = *reinterpret_cast<const uint2*>(base + i * Y::kRecord + 16 * D + 128 + (g + 8 * h) * 8);
-        const bool in = full || (key0 + 16 * i + g + 8 * h < sq.len && ((ok >> (2 * slot + i)) & 1u));
-        vs[i][h][0] = in ? bf16_lo(par.x) : 0.0f;
-        vm[i][h][0] = in ? bf16_hi(par.x) : 0.0f;
-        vs[i][h][1] = in ? bf16_lo(par.y) : 0.0f;
-        vm[i][h][1] = in ? bf16_hi(par.y) : 0.0f;
+        uint2 par = *reinterpret_cast<const uint2*>(base + i * Y::kRecord + 16 * D + 128 + (g + 8 * h) * 8);
+        if (!full && (key0 + 16 * i + g + 8 * h >= sq.len || !((ok >> (2 * slot + i)) & 1u))) par = make_uint2(0, 0);
+        vs[i][h][0] = bf16_lo(par.x);
+        vm[i][h][0] = bf16_hi(par.x);
+        vs[i][h][1] = bf16_lo(par.y);
+        vm[i][h][1] = bf16_hi(par.y);
       }
     float top[2];
 #pragma unroll
@@ -388,6 +399,9 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[ch][j][e] *= al[e & 1] * f[ch / CP];
     }
+    float mb[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mb[nt] = m_run[nt] == -INFINITY ? 0.0f : m_run[nt];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t pb[2][2];  // B operands of p s: plane, keys 0-7 / 8-15
@@ -397,7 +411,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
         float pr[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          pr[nt] = ex2(sc[i][nt][h] - (m_run[nt] == -INFINITY ? 0.0f : m_run[nt]));
+          pr[nt] = ex2(fmaf(sc[i][nt][h], cs[nt], -mb[nt]));
           l_run[nt] += pr[nt];
           pm[nt][0] = fmaf(pr[nt], vm[i][h][0], pm[nt][0]);
           pm[nt][1] = fmaf(pr[nt], vm[i][h][1], pm[nt][1]);
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const __grid_constan
       pm[nt][0] += __shfl_xor_sync(0xffffffffu, pm[nt][0], o);
       pm[nt][1] += __shfl_xor_sync(0xffffffffu, pm[nt][1], o);
     }
-    const int row = nt * 4 + t;
+    const int row = NT * t + nt;
     if (g == 0) mls[warp][row] = make_float2(m_run[nt], l_run[nt]);
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
