@@ -12,10 +12,11 @@
 //          terms (2^-22 of the row's largest entry): two neighbouring columns where a tile has up to 4
 //          query rows, two products into the same sums where it has 8
 //   K      score = scale sum_planes s (codes . q) + m sum(q), s and m of a key's plane, in float32
-//   P      p s 2^15 / cap as one fp16 term (2^-12 relative, 2^-40 of the cap absolute), cap a power of two
-//          above every s seen (raised, with the sums rescaled, when a larger one comes), transposed in
-//          registers (movmatrix) from the score layout into the B operand;
-//          o = sum_j (p s)_j codes_j + sum_j p_j m_j, the second sum in float32
+//   P      p = 2^(score - ref), ref the maximum when it was last raised: it is raised, and all sums rescaled,
+//          only when a score passes it by more than 2^kSlack, so that rescaling stays rare;
+//          p s 2^(15 - kSlack) / cap as one fp16 term (2^-11 relative), cap a power of two above every s
+//          seen (raised the same way), transposed in registers (movmatrix) from the score layout
+//          into the B operand; o = sum_j (p s)_j codes_j + sum_j p_j m_j, the second sum in float32
 // A lane holds the scores of one query row (of two, in tiles of 8) for the keys g and g + 8 of a record.
 //
 // Work split: (key/value head and tile of 8 query rows, sequence) x splits of the keys; the four warps of a
@@ -33,6 +34,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;                  // keys of a warp's step: two records
 constexpr int kStages = 2;
+constexpr int kSlack = 6;                  // how far (log2) a score may pass the reference
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 64;
 
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
     m_run[nt] = -INFINITY;
     l_run[nt] = pm[nt][0] = pm[nt][1] = 0.0f;
   }
-  float cap[2] = {0.0f, 0.0f}, to_w[2] = {0.0f, 0.0f};  // per plane: the cap on s, 2^15 / cap
+  float cap[2] = {0.0f, 0.0f}, to_w[2] = {0.0f, 0.0f};  // per plane: the cap on s, 2^(15 - kSlack) / cap
 
   const uint8_t* stage0 = smem + warp * kStages * Y::kStage;
   auto unit = [&](int slot, int32_t key0) {
@@ -346,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      mn[nt] = fmaxf(m_run[nt], mx * cs[nt]);
-      grew |= mn[nt] > m_run[nt];
+      mn[nt] = mx * cs[nt];
+      grew |= mn[nt] > m_run[nt] + kSlack;
     }
     // the values' scales and minima of this lane's keys: {record, key, plane}; 0 for keys that do not exist
     float vs[2][2][2], vm[2][2][2];
@@ -380,12 +382,13 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
           const int e = min(max((__float_as_int(mx) >> 23) - 127 + 2, -100), 126);  // mx < 2^(e - 1): room to grow
           f[pl] = cap[pl] * pow2(-e);
           cap[pl] = pow2(e);
-          to_w[pl] = pow2(15 - e);
+          to_w[pl] = pow2(15 - kSlack - e);
         }
       }
       float al[2] = {1.0f, 1.0f};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        mn[nt] = fmaxf(mn[nt], m_run[nt]);
         al[nt] = mn[nt] == -INFINITY ? 1.0f : ex2(m_run[nt] - mn[nt]);
         m_run[nt] = mn[nt];
         l_run[nt] *= al[nt];
@@ -450,6 +453,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
 
   // the warps' parts, then their sum, then the cluster's
   float* os = reinterpret_cast<float*>(smem);  // [warp][row][D]
+  // undo the codes' 2^-24 (2^-20 in the second half of the instruction's rows) and the weights' scaling
+  constexpr float kLow = (float)(1 << (9 + kSlack)), kHigh = (float)(1 << (5 + kSlack));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -464,10 +469,10 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
     for (int ch = 0; ch < CH; ++ch) {
       const float pmv = pm[nt][ch / CP], k = cap[ch / CP];
       float4 v;
-      v.x = fmaf(acc[ch][0][nt] * 0x1p9f, k, pmv);
-      v.y = fmaf(acc[ch][0][2 + nt] * 0x1p5f, k, pmv);
-      v.z = fmaf(acc[ch][1][nt] * 0x1p9f, k, pmv);
-      v.w = fmaf(acc[ch][1][2 + nt] * 0x1p5f, k, pmv);
+      v.x = fmaf(acc[ch][0][nt] * kLow, k, pmv);
+      v.y = fmaf(acc[ch][0][2 + nt] * kHigh, k, pmv);
+      v.z = fmaf(acc[ch][1][nt] * kLow, k, pmv);
+      v.w = fmaf(acc[ch][1][2 + nt] * kHigh, k, pmv);
       *reinterpret_cast<float4*>(&os[(warp * QR + row) * D + ch * 32 + 4 * g]) = v;
     }
   }

@@ -157,9 +157,9 @@ def kv4_attention(q, k, v, first, scale):
         p /= p.sum()
         o[i] = p @ vv[seen[i]]
         # a score off by d moves a weight by the factor exp(2 d) at most (its own and the sum's); the weights'
-        # rounding to fp16 2^-11, or 2^-25 of 2^15 / cap where subnormal, the cap at most 8 times the largest scale;
+        # rounding to fp16 2^-11, or 2^-25 of 2^9 / cap where subnormal, the cap at most 8 times the largest scale;
         # float32 sums over the keys, exp2 and the joins of partial results
         rel = np.expm1(2 * di.max()) + 2.0 ** -11 + (len(si) / 16 + 64) * 2.0 ** -22
-        flush = 2.0 ** -37 * 15 * len(si) * bf16_value(v[1][:len(si)]).max() / np.exp(si - si.max()).sum()
+        flush = 2.0 ** -31 * 15 * len(si) * bf16_value(v[1][:len(si)]).max() / np.exp(si - si.max()).sum()
         bound[i] = rel * (p @ va[seen[i]]) + flush
     return o, bound
