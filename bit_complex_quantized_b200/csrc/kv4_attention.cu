@@ -36,7 +36,9 @@ constexpr int kUnit = 32;                  // keys of a warp's step: two records
 constexpr int kStages = 2;
 constexpr int kSlack = 6;                  // how far (log2) a score may pass the reference
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSplits = 64;
+
+// CTAs that an SM holds (its registers decide).
+__host__ __device__ constexpr int ctas_per_sm(int dim, int nt) { return dim == 128 ? 2 : dim == 64 && nt == 2 ? 3 : 4; }
 
 struct AttnParams {
   Kv4Arg c;
@@ -46,6 +48,7 @@ struct AttnParams {
   float scale2;      // scale log2 e
   int32_t shared;    // query heads of a key/value head
   int32_t splits, cluster, qtiles;
+  int32_t by_length; // the longest sequences' CTAs start first
   float* ws_o;       // [B][kv_heads][qtiles QR][splits / cluster][D]
   float2* ws_ml;     // [B][kv_heads][qtiles QR][splits / cluster]: maximum (log2), sum
   uint32_t* status;
@@ -131,7 +134,7 @@ struct Layout {
 };
 
 template <int DIM, int NT>
-__global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT)) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
   using Y = Layout<DIM, NT>;
   constexpr int D = Y::D, CH = Y::CH, CP = DIM / 32, QR = Y::QR, T4 = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -141,8 +144,23 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
   __shared__ float2 ml_cta[QR];
   uint4* qs = reinterpret_cast<uint4*>(smem + Y::kRing);
   const Kv4Arg& c = p.c;
-  const int b = blockIdx.z, kvh = blockIdx.y / p.qtiles, qt = blockIdx.y % p.qtiles;
+  const int kvh = blockIdx.y / p.qtiles, qt = blockIdx.y % p.qtiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  int b = blockIdx.z;
+  if (p.by_length) {  // the sequence whose length is the blockIdx.z-th largest (ties in their order)
+    int* lens = reinterpret_cast<int*>(smem);
+    __shared__ int chosen;
+    const int i = threadIdx.x, len = i < c.B ? __ldg(c.kv_lens + i) : 0;
+    if (i < c.B) lens[i] = len;
+    __syncthreads();
+    if (i < c.B) {
+      int at = 0;
+      for (int j = 0; j < c.B; ++j) at += lens[j] > len || (lens[j] == len && j < i);
+      if (at == b) chosen = i;
+    }
+    __syncthreads();
+    b = chosen;
+  }
   const Kv4Seq sq = kv4_seq(c, b);
   if (!sq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   const int nrows = sq.n_new * p.shared - qt * QR;  // query rows of this tile
@@ -169,11 +187,22 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
   };
   uint32_t rec_now = fetch(t_begin), rec_next = fetch(t_begin + 32);
   const uint32_t ring = smem_u32(smem) + warp * kStages * Y::kStage + lane * 16;
+  const bool even_pages = (c.page_tiles & 1) == 0;  // the two records of a step are neighbours in a page
   uint32_t ok = 0;          // bit 2 slot + i: record i of the slot's stage is there
   int32_t tl = t_begin;     // first tile of the next load
   auto load = [&](int slot) {
     if (tl < t_end) {
       ok &= ~(3u << (2 * slot));
+      if (even_pages && tl + 1 < t_end) {
+        const uint32_t r = __shfl_sync(0xffffffffu, rec_now, (tl - t_begin) & 31);
+        if (r != 0xFFFFFFFFu) {
+          ok |= 3u << (2 * slot);
+          const uint8_t* src = c.records + (uint64_t)r * Y::kRecord + lane * 16;
+          const uint32_t dst = ring + slot * Y::kStage;
+#pragma unroll
+          for (int v = 0; v < Y::kStage / 512; ++v) cp_async16(dst + v * 512, src + v * 512);
+        }
+      } else
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t r = __shfl_sync(0xffffffffu, rec_now, (tl - t_begin + i) & 31);
@@ -197,63 +226,56 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
 #pragma unroll
   for (int st = 0; st < kStages - 1; ++st) load(st);
 
-  // q: a row's largest exponent and plane sums (a warp per row), then the operands
-  auto q_row = [&](int row, int d) -> const float* {
-    const int rr = qt * QR + row, tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
-    return p.q[d / DIM] + (sq.row0 + tok) * p.ldq + head * DIM + d % DIM;
-  };
+  // q, a warp per row: lane l has the entries E l .. E l + E - 1.  The row's exponent, its plane sums, and its two
+  // fp16 terms at their places in the operands.
+  constexpr int E = D / 32;
   for (int row = warp; row < QR; row += kWarps) {
-    float mx = 0.0f, sum[2] = {};
-    bool bad = false;
-    if (row < nrows)
+    float v[E] = {};
+    if (row < nrows) {
+      const int rr = qt * QR + row, tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
+      const float* src = p.q[lane / 16] + (sq.row0 + tok) * p.ldq + head * DIM + lane % 16 * E;
 #pragma unroll
-      for (int d = lane * 2; d < D; d += 64) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(q_row(row, d)));
-        mx = fmaxf(mx, fmaxf(fabsf(v.x * p.scale2), fabsf(v.y * p.scale2)));
-        bad |= !(fabsf(v.x) <= 3.402823466e38f) || !(fabsf(v.y) <= 3.402823466e38f);
+      for (int j = 0; j < E; j += 2) {
+        const float2 x = __ldg(reinterpret_cast<const float2*>(src + j));
+        v[j] = x.x;
+        v[j + 1] = x.y;
       }
+    }
+    float mx = 0.0f, sum = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      bad |= !(fabsf(v[j]) <= 3.402823466e38f);
+      v[j] *= p.scale2;
+      mx = fmaxf(mx, fabsf(v[j]));
+    }
     if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     // mx < 2^(e + 1); a zero or subnormal row keeps the smallest exponent, an infinite one becomes NaN below
     const int e = max((__float_as_int(mx) >> 23) - 127, -100);
-    const float f = pow2(min(14 - e, 127)) ;
-    if (row < nrows)
+    const float f = pow2(14 - e);
 #pragma unroll
-      for (int d = lane * 2; d < D; d += 64) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(q_row(row, d)));
-        sum[d / DIM] += f * (v.x * p.scale2) + f * (v.y * p.scale2);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+    for (int j = 0; j < E; ++j) {
+      v[j] *= f;
+      sum += v[j];
+      if ((lane * E + j) & 2) v[j] *= 0x1p-4f;  // entries 2, 3, 6, 7 of a word meet codes times 16
     }
-    if (lane == 0) {
-      qexp[row] = e;
-      qsum[row][0] = sum[0] * 0x1p-24f;
-      qsum[row][1] = sum[1] * 0x1p-24f;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < NT * CH * 32; i += kThreads) {
-    const int ln = i & 31, ch = (i >> 5) % CH;
-    const int row = NT == 1 ? ln >> 3 : ln >> 2, part = NT == 1 ? (ln >> 2) & 1 : (i >> 5) / CH;
-    uint32_t w[4] = {};
-    if (row < nrows) {
-      const float4* src = reinterpret_cast<const float4*>(q_row(row, ch * 32 + (ln & 3) * 8));
-      const float f = pow2(min(14 - qexp[row], 127));
-      const float4 a = __ldg(src), bq = __ldg(src + 1);
-      float v[8] = {a.x, a.y, a.z, a.w, bq.x, bq.y, bq.z, bq.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = v[j] * p.scale2 * ((j & 2) ? f * 0x1p-4f : f);  // entries 2, 3, 6, 7 meet codes times 16
-        if (part) v[j] -= __half2float(__float2half_rn(v[j]));
-      }
+    for (int o = 8; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) qexp[row] = e;
+    if (lane % 16 == 0) qsum[row][lane / 16] = sum * 0x1p-24f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < E; j += 2) {
+      const int d = lane * E + j, ch = d >> 5, tt = (d & 31) >> 3;
+      const uint32_t hi = pack_f16(v[j], v[j + 1]);
+      const __half2 h2 = *reinterpret_cast<const __half2*>(&hi);
+      const uint32_t lo = pack_f16(v[j] - __low2float(h2), v[j + 1] - __high2float(h2));
+      // term p of row r: column 2 r + p of the one n tile, or column r of tile p
+      uint32_t* q0 = reinterpret_cast<uint32_t*>(qs + ch * 32 + (NT == 1 ? 8 * row : 4 * row) + tt) + ((d & 7) >> 1);
+      q0[0] = hi;
+      q0[NT == 1 ? 16 : CH * 128] = lo;
     }
-    qs[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncthreads();
 
@@ -340,15 +362,11 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
           for (int h = 0; h < 2; ++h)
             if (key0 + 16 * i + g + 8 * h >= visible[nt] || !((ok >> (2 * slot + i)) & 1u)) sc[i][nt][h] = -INFINITY;
     }
-    float mn[NT];
+    float mn[NT];  // this lane's largest score of a row
     bool grew = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx = fmaxf(fmaxf(sc[0][nt][0], sc[0][nt][1]), fmaxf(sc[1][nt][0], sc[1][nt][1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      mn[nt] = mx * cs[nt];
+      mn[nt] = cs[nt] * fmaxf(fmaxf(sc[0][nt][0], sc[0][nt][1]), fmaxf(sc[1][nt][0], sc[1][nt][1]));
       grew |= mn[nt] > m_run[nt] + kSlack;
     }
     // the values' scales and minima of this lane's keys: {record, key, plane}; 0 for keys that do not exist
@@ -388,6 +406,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
       float al[2] = {1.0f, 1.0f};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) mn[nt] = fmaxf(mn[nt], __shfl_xor_sync(0xffffffffu, mn[nt], o));
         mn[nt] = fmaxf(mn[nt], m_run[nt]);
         al[nt] = mn[nt] == -INFINITY ? 1.0f : ex2(m_run[nt] - mn[nt]);
         m_run[nt] = mn[nt];
@@ -538,59 +558,76 @@ __global__ void __launch_bounds__(kThreads, DIM == 128 ? 2 : 4) kv4_attn_kernel(
   cluster_sync();  // no CTA leaves while its sums are being read
 }
 
-// The groups of splits of a query row, added in their order.  One warp per query row.
+// The groups of splits of a query row, added in a fixed order.  A CTA per query row: its warps take the groups
+// in turn, four at a time in flight, and are then added in their order.
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const __grid_constant__ AttnParams p, int qr) {
   constexpr int D = 2 * DIM;
+  __shared__ float os[kWarps][D];
+  __shared__ float ls[kWarps];
   const Kv4Arg& c = p.c;
-  const int lane = threadIdx.x & 31, b = blockIdx.z, kvh = blockIdx.y;
-  const int rr = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.z, kvh = blockIdx.y, rr = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the main kernel ends
   const Kv4Seq sq = kv4_seq(c, b);
   if (rr >= sq.n_new * p.shared) return;
   const int used = used_groups(sq.len, p.splits, p.cluster);
   const int64_t at = (((int64_t)b * c.kv_heads + kvh) * p.qtiles * qr + rr) * (p.splits / p.cluster);
   float M = -INFINITY;
-  for (int s = 0; s < used; ++s) M = fmaxf(M, p.ws_ml[at + s].x);
+  for (int s = lane; s < used; s += 32) M = fmaxf(M, __ldcg(p.ws_ml + at + s).x);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ms = M == -INFINITY ? 0.0f : M;
   float l = 0.0f;
   float2 o[D / 64] = {};
-  for (int s = 0; s < used; ++s) {
-    const float2 ml = p.ws_ml[at + s];
+#pragma unroll 4
+  for (int s = warp; s < used; s += kWarps) {
+    const float2 ml = __ldcg(p.ws_ml + at + s);
     const float f = ex2(ml.x - ms);
     l += f * ml.y;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-      const float2 v = *reinterpret_cast<const float2*>(p.ws_o + (at + s) * D + i * 64 + lane * 2);
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws_o + (at + s) * D + i * 64 + lane * 2));
       o[i].x += f * v.x;
       o[i].y += f * v.y;
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int d = i * 64 + lane * 2;
-    *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (sq.row0 + tok) * p.ldo + head * DIM + d % DIM) =
-        pack_bf16(o[i].x * inv, o[i].y * inv);
-  }
+  for (int i = 0; i < D / 64; ++i) *reinterpret_cast<float2*>(&os[warp][i * 64 + lane * 2]) = o[i];
+  if (lane == 0) ls[warp] = l;
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  const int d = threadIdx.x * 2;
+  l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float o0 = (os[0][d] + os[1][d]) + (os[2][d] + os[3][d]);
+  const float o1 = (os[0][d + 1] + os[1][d + 1]) + (os[2][d + 1] + os[3][d + 1]);
+  const int tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
+  *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (sq.row0 + tok) * p.ldo + head * DIM + d % DIM) =
+      pack_bf16(o0 * inv, o1 * inv);
 }
 
 struct Plan {
-  int nt, qtiles, splits, cluster;
+  int nt, qtiles, splits, cluster, by_length;
 };
 
-// Two n tiles (8 query rows) where there are more than 4 query rows.  Splits, a power of two: until the CTAs
-// fill the GPU or a warp would have less than one step of the longest sequence that the table can hold.
+// CTAs of 8 query rows where there are more than 4.  Splits: as many as the GPU holds CTAs at once, but a warp
+// has at least one step of the longest sequence that the table can hold.  Up to 8 splits are one cluster, joined in
+// the same launch; more are joined by the second kernel.  Several sequences are cut into 4 parts at least, since
+// their lengths differ, and start in the order of their lengths where they do not all fit at once.
 Plan plan(const ifq_kv4_cache& c, int shared) {
   Plan r;
   const int64_t rows = (int64_t)c.n_new * shared;
   r.nt = rows > 4 ? 2 : 1;
   r.qtiles = (int)((rows + 4 * r.nt - 1) / (4 * r.nt));
-  const int64_t ctas = (int64_t)c.B * c.kv_heads * r.qtiles;
-  const int64_t keys = c.table_cols * c.page_tokens;
-  r.splits = 1;
-  while (r.splits < kMaxSplits && ctas * r.splits < 148 * 4 && (int64_t)r.splits * kWarps * kUnit < keys) r.splits *= 2;
-  r.cluster = r.splits < kMaxCluster ? r.splits : kMaxCluster;
+  const int64_t ctas = (int64_t)c.B * c.kv_heads * r.qtiles, slots = 148 * ctas_per_sm(c.dim, r.nt);
+  const int64_t most = (c.table_cols * c.page_tokens + kWarps * kUnit - 1) / (kWarps * kUnit);
+  int64_t s = slots / ctas;
+  if (c.B > 1 && s < 4) s = 4;
+  if (s > most) s = most;
+  if (s <= kMaxCluster) s = s >= 8 ? 8 : s >= 4 ? 4 : s >= 2 ? 2 : 1;
+  r.splits = (int)s;
+  r.cluster = s <= kMaxCluster ? (int)s : 1;
+  r.by_length = c.B > 1 && c.B <= kThreads && ctas * s > slots;
   return r;
 }
 
@@ -635,9 +672,17 @@ template <int DIM>
 cudaError_t launch(const AttnParams& p, const Plan& r, cudaStream_t s) {
   cudaError_t e = r.nt == 1 ? launch_nt<DIM, 1>(p, s) : launch_nt<DIM, 2>(p, s);
   if (e != cudaSuccess || r.splits == r.cluster) return e;
-  const dim3 mg((unsigned)((p.c.n_new * p.shared + kWarps - 1) / kWarps), (unsigned)p.c.kv_heads, (unsigned)p.c.B);
-  kv4_merge_kernel<DIM><<<mg, kThreads, 0, s>>>(p, 4 * r.nt);
-  return cudaGetLastError();
+  const dim3 mg((unsigned)(p.c.n_new * p.shared), (unsigned)p.c.kv_heads, (unsigned)p.c.B);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = mg;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<DIM>, p, 4 * r.nt);
 }
 
 }  // namespace
@@ -665,6 +710,7 @@ cudaError_t launch_kv4_attention(const ifq_kv4_cache& c, int shared, const float
   p.splits = r.splits;
   p.cluster = r.cluster;
   p.qtiles = r.qtiles;
+  p.by_length = r.by_length;
   p.ws_o = static_cast<float*>(ws);
   p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + partials(c, r) * 2 * c.dim);
   p.status = dev_status;
