@@ -5,15 +5,22 @@
 // that no range overflows), n = rint((x - m) / s) half-even of the exact quotient, clamped to [0, 15], 0 where s = 0.
 // The stored value is s n + m.  Codes are chosen against the rounded s and m.
 //
-// A thread takes 8 entries; dim / 8 neighbouring threads hold a plane and reduce its minimum and
-// maximum by shuffles.
+// Two forms.  Fewer than 16 new tokens a sequence (decode): a thread takes 8 entries of a token, dim / 8
+// neighbouring threads a plane, and writes its words and half words alone: as many threads as there are entries, the
+// shortest chain.  More (prompts): a warp takes one record (16 tokens of a head): keys as lane (g, t) holds them in the record (8 entries
+// of the tokens g and g + 8 per 32 columns), values likewise (4 entries of four tokens), so that loads
+// are 128-byte runs, a plane's minimum and maximum take two or three shuffles, and a record that is
+// all new leaves as 512-byte stores.  A record that holds older tokens too is written token by token: a token's keys
+// are whole words and its values whole half words, so nothing is read back.  HBM-bound: 16 dim bytes read and 2 dim + 16
+// written per token and head.
 #include "ifq_internal.h"
 #include "kv4_common.cuh"
 
 namespace ifq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 
 struct AppendParams {
   Kv4Arg c;
@@ -25,24 +32,88 @@ struct AppendParams {
 
 constexpr float kBf16Max = 3.3895313892515355e38f;
 
-// n = rint((x - m) / s), exact: d + e = x - m (two-term sum), the quotient of d decides except next to
-// a half, where the residual d - s n0 (exact in float32) plus e is compared with s / 2.
-IFQ_DEVINL uint32_t kv4_code(float x, float s, float m, float inv) {
-  const float d = x - m;
-  const float bb = d - x;
-  const float e = (x - (d - bb)) - (m + bb);
-  float n0 = rintf(s >= 1e-30f ? d * inv : d / s);
-  n0 = fminf(fmaxf(n0, 0.0f), 15.0f);
-  const float f = fmaf(-s, n0, d), h = 0.5f * s;
-  const bool odd = ((int)n0 & 1) != 0;
-  const float up = (f - h) + e, dn = (f + h) + e;   // f +- h is exact next to the half
-  if (up > 0.0f || (up == 0.0f && odd)) n0 += 1.0f;
-  else if (dn < 0.0f || (dn == 0.0f && odd)) n0 -= 1.0f;
-  return (uint32_t)fminf(fmaxf(n0, 0.0f), 15.0f);
+// The record of a warp: its address (null: none), its first position, the sequence.
+struct Item {
+  uint8_t* rec;
+  int32_t pos0, first;  // position of the record's token 0; first new position
+  Kv4Seq q;
+  int head;
+};
+
+IFQ_DEVINL bool find_item(const AppendParams& p, Item* it) {
+  const Kv4Arg& c = p.c;
+  const int b = blockIdx.y;
+  it->q = kv4_seq(c, b);
+  if (!it->q.ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
+  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  it->head = (int)(item % c.kv_heads);
+  // a sequence whose length is unusable has no positions, but its rows still read as 0
+  const int32_t len = it->q.ok ? it->q.len : it->q.n_new;
+  it->first = len - it->q.n_new;
+  const int64_t tile = (it->first >> 4) + item / c.kv_heads;
+  if (tile * 16 >= len) return false;
+  it->pos0 = (int32_t)tile * 16;
+  it->rec = nullptr;
+  if (it->q.ok) {
+    it->rec = kv4_record(c, b, it->head, (int32_t)tile);
+    if (!it->rec && (threadIdx.x & 31) == 0) set_status(p.status, IFQ_DEV_RANGE);
+  }
+  return true;
 }
 
+struct Group {  // a plane's parameters
+  float s, m, inv;
+  uint32_t bits;
+  bool fast;
+};
+IFQ_DEVINL Group group_of(float lo, float hi) {
+  const __nv_bfloat16 mb = __float2bfloat16_rn(lo);
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__fsub_rn(__fmul_rn(hi, 1.0f / 15.0f), __fmul_rn(lo, 1.0f / 15.0f)));
+  Group r;
+  r.s = __bfloat162float(sb);
+  r.m = __bfloat162float(mb);
+  r.inv = code_reciprocal(r.s, &r.fast);
+  r.bits = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
+  return r;
+}
+// Entry j of four in bits 4 j.
+IFQ_DEVINL uint32_t codes_of(const float4& x, const Group& q) {
+  bool near = !q.fast;
+  const uint32_t w = fast_codes4(x, q.m, q.inv, 0.0f, 15.0f, 0.0f, &near);
+  return near ? exact_codes4(x, q.s, q.m, 0.0f, 15.0f, 0.0f) : w;
+}
+// The word of eight entries of a key: entries 0, 2, 4, 6 in the low half, 1, 3, 5, 7 in the high half.
+IFQ_DEVINL uint32_t key_word(const float4& a, const float4& b, const Group& q) {
+  return codes_of(make_float4(a.x, a.z, b.x, b.z), q) | (codes_of(make_float4(a.y, a.w, b.y, b.w), q) << 16);
+}
+
+IFQ_DEVINL float4 take(const float* src, bool in) {
+  return in ? __ldcs(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+// Minimum and maximum so far; odd becomes NaN with a NaN or Inf entry.
+IFQ_DEVINL void widen(const float4& v, float* lo, float* hi, float* odd) {
+  *lo = fminf(*lo, fminf(fminf(v.x, v.y), fminf(v.z, v.w)));
+  *hi = fmaxf(*hi, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+  *odd = fmaf(v.x, 0.0f, fmaf(v.y, 0.0f, fmaf(v.z, 0.0f, fmaf(v.w, 0.0f, *odd))));
+}
+// NaN and Inf become 0 (*bad), larger magnitudes the largest bf16.
+IFQ_DEVINL void tame(float4& v, bool* bad) {
+  float* f = &v.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (!(fabsf(f[j]) <= 3.402823466e38f)) {
+      f[j] = 0.0f;
+      *bad = true;
+    }
+    f[j] = fminf(fmaxf(f[j], -kBf16Max), kBf16Max);
+  }
+}
+// Whether a lane's entries need tame().
+IFQ_DEVINL bool wild(float lo, float hi, float odd) { return !(odd == 0.0f) || lo < -kBf16Max || hi > kBf16Max; }
+
+// One token's plane, 8 entries a thread.
 template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads) kv4_append_tokens_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LP = DIM / 8, D = 2 * DIM;
   const Kv4Arg& c = p.c;
   const int b = blockIdx.y;
@@ -51,30 +122,26 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
     return;
   }
-  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int part = (int)(idx % LP), plane = (int)(idx / LP) & 3;
-  const int64_t th = idx / (4 * LP);
-  const int head = (int)(th % c.kv_heads);
-  const int64_t tok = th / c.kv_heads;
+  const int idx = blockIdx.x * kThreads + threadIdx.x;  // below 16 x 1024 x 64
+  const int part = idx % LP, plane = (idx / LP) & 3, th = idx / (4 * LP);
+  const int head = th % c.kv_heads, tok = th / c.kv_heads;
   const bool live = tok < q.n_new;
-  float x[8] = {};
+  const int32_t pos = q.len - q.n_new + tok;
+  uint8_t* rec = live ? kv4_record(c, b, head, pos >> 4) : nullptr;
+  float4 x[2];
+  const float* src = p.src[plane] + (q.row0 + tok) * p.ld + head * DIM + part * 8;
+  x[0] = take(src, live);
+  x[1] = take(src + 4, live);
+  float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
+  widen(x[0], &lo, &hi, &odd);
+  widen(x[1], &lo, &hi, &odd);
   bool bad = false;
-  if (live) {
-    const float4* src = reinterpret_cast<const float4*>(p.src[plane] + (q.row0 + tok) * p.ld + head * DIM + part * 8);
-    const float4 a = __ldcs(src), bq = __ldcs(src + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = bq.x; x[5] = bq.y; x[6] = bq.z; x[7] = bq.w;
-  }
-  float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (!(fabsf(x[j]) <= 3.402823466e38f)) {
-      x[j] = 0.0f;
-      bad = true;
-    }
-    x[j] = fminf(fmaxf(x[j], -kBf16Max), kBf16Max);
-    lo = fminf(lo, x[j]);
-    hi = fmaxf(hi, x[j]);
+  if (wild(lo, hi, odd)) {
+    tame(x[0], &bad);
+    tame(x[1], &bad);
+    lo = INFINITY, hi = -INFINITY;
+    widen(x[0], &lo, &hi, &odd);
+    widen(x[1], &lo, &hi, &odd);
   }
 #pragma unroll
   for (int o = 1; o < LP; o *= 2) {
@@ -83,54 +150,216 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_const
   }
   if (!live) return;
   if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
-  const __nv_bfloat16 mb = __float2bfloat16_rn(lo);
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fsub_rn(__fmul_rn(hi, 1.0f / 15.0f), __fmul_rn(lo, 1.0f / 15.0f)));
-  const float s = __bfloat162float(sb), m = __bfloat162float(mb);
-  const float inv = s >= 1e-30f ? __frcp_rn(s) : 0.0f;
-  uint32_t n[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) n[j] = s > 0.0f ? kv4_code(x[j], s, m, inv) : 0u;
-
-  const int32_t pos = q.len - q.n_new + (int32_t)tok;
-  uint8_t* rec = kv4_record(c, b, head, pos >> 4);
   if (!rec) {
     if (part == 0) set_status(p.status, IFQ_DEV_RANGE);
     return;
   }
-  const int r = pos & 15, hh = r >> 3;
-  const int d = (plane & 1) * DIM + part * 8;  // first of the 8 stacked entries
+  const Group gq = group_of(lo, hi);
+  const int r = pos & 15, hh = r >> 3, d = (plane & 1) * DIM + part * 8;  // d: first of the 8 stacked entries
   if (plane < 2) {
     uint32_t* w = reinterpret_cast<uint32_t*>(rec + (d >> 6) * 512 + (((r & 7) * 4 + ((d & 31) >> 3)) << 4));
-    w[((d & 63) >> 5) * 2 + hh] = q4_pack_word(n);
+    w[((d & 63) >> 5) * 2 + hh] = key_word(x[0], x[1], gq);
   } else {
     const int qb = d >> 5, g = (d & 31) >> 2, t = (r & 7) >> 1;
     uint8_t* base = rec + 8 * D + (qb >> 1) * 512 + ((qb & 1) * 2 + hh) * 4 + (r & 1) * 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint16_t*>(base + (((g + i) * 4 + t) << 4)) =
-          (uint16_t)(n[4 * i] | (n[4 * i + 1] << 4) | (n[4 * i + 2] << 8) | (n[4 * i + 3] << 12));
+      *reinterpret_cast<uint16_t*>(base + (((g + i) * 4 + t) << 4)) = (uint16_t)codes_of(x[i], gq);
   }
-  if (part == 0)
-    *reinterpret_cast<uint32_t*>(rec + 16 * D + (plane >> 1) * 128 + r * 8 + (plane & 1) * 4) =
-        (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
+  if (part == 0) *reinterpret_cast<uint32_t*>(rec + 16 * D + (plane >> 1) * 128 + r * 8 + (plane & 1) * 4) = gq.bits;
 }
 
 template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int D = 2 * DIM, CH = D / 32, CP = DIM / 32;
+  Item it;
+  if (!find_item(p, &it) || !it.rec) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int32_t len = it.q.len;
+  auto in = [&](int r) { return it.pos0 + r >= it.first && it.pos0 + r < len; };
+  auto row = [&](const float* base, int r) {
+    return base + (it.q.row0 + it.pos0 + r - it.first) * p.ld + it.head * DIM;
+  };
+  const bool all = in(0) && in(15);
+  bool bad = false;
+  uint32_t* par = reinterpret_cast<uint32_t*>(it.rec + 16 * D);
+
+  uint32_t words[CH][2];  // {32-column chunk, token g or g + 8}
+#pragma unroll
+  for (int pl = 0; pl < 2; ++pl) {
+    float4 v[2][CP][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < CP; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[h][c][i] = take(row(p.src[pl], g + 8 * h) + c * 32 + t * 8 + i * 4, in(g + 8 * h));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CP; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) widen(v[h][c][i], &lo, &hi, &odd);
+      if (wild(lo, hi, odd)) {
+        lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tame(v[h][c][i], &bad);
+            widen(v[h][c][i], &lo, &hi, &odd);
+          }
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      const Group q = group_of(lo, hi);
+#pragma unroll
+      for (int c = 0; c < CP; ++c) words[pl * CP + c][h] = key_word(v[h][c][0], v[h][c][1], q);
+      if (t == 0 && in(g + 8 * h)) par[(g + 8 * h) * 2 + pl] = q.bits;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CH / 2; ++k) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(it.rec + k * 512 + lane * 16);
+    if (all) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(words[2 * k][0], words[2 * k][1], words[2 * k + 1][0], words[2 * k + 1][1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (in(g + 8 * (e & 1))) dst[e] = words[2 * k + (e >> 1)][e & 1];
+    }
+  }
+
+  // values: {32-column chunk, tokens 2 t + 8 h and 2 t + 8 h + 1}
+#pragma unroll
+  for (int pl = 0; pl < 2; ++pl) {
+    float4 v[2][2][CP];  // {h, token of the pair, chunk}: entries 4 g .. 4 g + 3
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < CP; ++c) {
+          const int r = 2 * t + 8 * h + e;
+          v[h][e][c] = take(row(p.src[2 + pl], r) + c * 32 + g * 4, in(r));
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * t + 8 * h + e;
+        float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CP; ++c) widen(v[h][e][c], &lo, &hi, &odd);
+        if (wild(lo, hi, odd)) {
+          lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < CP; ++c) {
+            tame(v[h][e][c], &bad);
+            widen(v[h][e][c], &lo, &hi, &odd);
+          }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2) {
+          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        const Group q = group_of(lo, hi);
+#pragma unroll
+        for (int c = 0; c < CP; ++c) {
+          const uint32_t w = codes_of(v[h][e][c], q) << (16 * e);
+          words[pl * CP + c][h] = e == 0 ? w : words[pl * CP + c][h] | w;
+        }
+        if (g == 0 && in(r)) par[32 + r * 2 + pl] = q.bits;
+      }
+  }
+#pragma unroll
+  for (int k = 0; k < CH / 2; ++k) {
+    uint8_t* dst = it.rec + 8 * D + k * 512 + lane * 16;
+    if (all) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(words[2 * k][0], words[2 * k][1], words[2 * k + 1][0], words[2 * k + 1][1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)  // half words: token 2 t + 8 h + (e & 1)
+        if (in(2 * t + 8 * ((e >> 1) & 1) + (e & 1)))
+          reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(words[2 * k + (e >> 2)][(e >> 1) & 1] >> (16 * (e & 1)));
+    }
+  }
+  if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kThreads) kv4_read_records_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int D = 2 * DIM, CH = D / 32, CP = DIM / 32;
+  Item it;
+  if (!find_item(p, &it)) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int32_t end = it.first + it.q.n_new;
+  auto in = [&](int r) { return it.pos0 + r >= it.first && it.pos0 + r < end; };
+  auto row = [&](float* base, int r) { return base + (it.q.row0 + it.pos0 + r - it.first) * p.ld + it.head * DIM; };
+  auto put = [&](float* dst, uint32_t sm, const uint32_t (&n)[4]) {
+    const float s = bf16_lo(sm), m = bf16_hi(sm);
+    __stcs(reinterpret_cast<float4*>(dst),
+           make_float4(fmaf(s, (float)n[0], m), fmaf(s, (float)n[1], m), fmaf(s, (float)n[2], m), fmaf(s, (float)n[3], m)));
+  };
+  const uint32_t* par = reinterpret_cast<const uint32_t*>(it.rec + 16 * D);
+  uint4 kv[2][CH / 2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int k = 0; k < CH / 2; ++k) {
+      kv[x][k] = make_uint4(0, 0, 0, 0);
+      if (it.rec) kv[x][k] = *reinterpret_cast<const uint4*>(it.rec + x * 8 * D + k * 512 + lane * 16);
+    }
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch) {
+    const int pl = ch / CP;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4& kq = kv[0][ch / 2];
+      const uint4& vq = kv[1][ch / 2];
+      const uint32_t kw = ch & 1 ? (h ? kq.w : kq.z) : (h ? kq.y : kq.x);
+      const uint32_t vw = ch & 1 ? (h ? vq.w : vq.z) : (h ? vq.y : vq.x);
+      const int rk = g + 8 * h;
+      if (in(rk)) {
+        const uint32_t sm = it.rec ? par[rk * 2 + pl] : 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t n[4] = {(kw >> (8 * i)) & 15u, (kw >> (16 + 8 * i)) & 15u, (kw >> (4 + 8 * i)) & 15u,
+                                 (kw >> (20 + 8 * i)) & 15u};
+          put(row(p.dst[pl], rk) + (ch % CP) * 32 + t * 8 + i * 4, sm, n);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rv = 2 * t + 8 * h + e;
+        if (!in(rv)) continue;
+        const uint32_t sm = it.rec ? par[32 + rv * 2 + pl] : 0u, w = vw >> (16 * e);
+        const uint32_t n[4] = {w & 15u, (w >> 4) & 15u, (w >> 8) & 15u, (w >> 12) & 15u};
+        put(row(p.dst[2 + pl], rv) + (ch % CP) * 32 + g * 4, sm, n);
+      }
+    }
+  }
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kThreads) kv4_read_tokens_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LP = DIM / 8, D = 2 * DIM;
   const Kv4Arg& c = p.c;
   const int b = blockIdx.y;
   const Kv4Seq q = kv4_seq(c, b);
   if (!q.ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
-  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int part = (int)(idx % LP), plane = (int)(idx / LP) & 3;
-  const int64_t th = idx / (4 * LP);
-  const int head = (int)(th % c.kv_heads);
-  const int64_t tok = th / c.kv_heads;
+  const int idx = blockIdx.x * kThreads + threadIdx.x;
+  const int part = idx % LP, plane = (idx / LP) & 3, th = idx / (4 * LP);
+  const int head = th % c.kv_heads, tok = th / c.kv_heads;
   if (tok >= q.n_new) return;
   float o[8] = {};
   uint8_t* rec = nullptr;
-  const int32_t pos = q.len - q.n_new + (int32_t)tok;
+  const int32_t pos = q.len - q.n_new + tok;
   if (q.ok) {
     rec = kv4_record(c, b, head, pos >> 4);
     if (!rec && part == 0) set_status(p.status, IFQ_DEV_RANGE);
@@ -163,10 +392,15 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const __grid_constan
 
 template <int DIM>
 cudaError_t launch(const AppendParams& p, bool read, cudaStream_t s) {
-  const int64_t threads = (int64_t)p.c.n_new * p.c.kv_heads * (DIM / 2);
-  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)p.c.B);
-  if (read) kv4_read_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
-  else kv4_append_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+  const bool tokens = p.c.n_new < 16;
+  // threads of 8 entries, or warps of the records that n_new tokens can touch
+  const int64_t blocks = tokens ? ((int64_t)p.c.n_new * p.c.kv_heads * (DIM / 2) + kThreads - 1) / kThreads
+                                : ((p.c.n_new + 14) / 16 + 1) * (int64_t)p.c.kv_heads / kWarps + 1;
+  const dim3 grid((unsigned)blocks, (unsigned)p.c.B);
+  if (tokens && read) kv4_read_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+  else if (tokens) kv4_append_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+  else if (read) kv4_read_records_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+  else kv4_append_records_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

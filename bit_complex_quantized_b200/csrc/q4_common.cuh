@@ -60,23 +60,51 @@ IFQ_DEVINL void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// The 8 codes (0..15) of a word, from its columns' codes.
-IFQ_DEVINL uint32_t q4_pack_word(const uint32_t (&n)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w |= n[j] << (4 * (j >> 1) + 16 * (j & 1));
-  return w;
+// rint((x - m) / s) half-even of the exact quotient, clamped to [lo, hi], for finite x and bf16 values s > 0, m.
+// d + e = x - m (two-term sum); the quotient of d decides except next to a half, where the residual d - s n
+// (exact in float32: both are multiples of one unit and it is at most 1.5 s) plus e is compared with s / 2.
+IFQ_DEVINL float exact_code(float x, float s, float m, float lo, float hi) {
+  const float d = x - m;
+  const float bb = d - x;
+  const float e = (x - (d - bb)) - (m + bb);
+  float n = fminf(fmaxf(rintf(d / s), lo), hi);
+  const float f = fmaf(-s, n, d), h = 0.5f * s;
+  const bool odd = ((int)n & 1) != 0;
+  const float up = (f - h) + e, dn = (f + h) + e;
+  if (up > 0.0f || (up == 0.0f && odd)) n += 1.0f;
+  else if (dn < 0.0f || (dn == 0.0f && odd)) n -= 1.0f;
+  return fminf(fmaxf(n, lo), hi);
 }
 
-// q = rint(v / s) half-even of the exact quotient, for s > 0 a bf16 value and |v / s| below 2^20.  The
-// product with a reciprocal may land one step off next to a half; the residual v - s q0 is exact in
-// float32 (both are multiples of one unit and it is at most 1.5 s), so comparing it with s / 2 decides.
-IFQ_DEVINL float q4_round_quotient(float v, float s, float inv) {
-  const float q0 = rintf(s >= 1e-30f ? v * inv : v / s);
-  const float f = fmaf(-s, q0, v);
-  const float a = fabsf(f), h = 0.5f * s;
-  const bool odd = ((int)q0 & 1) != 0;
-  return (a > h || (a == h && odd)) ? q0 + copysignf(1.0f, f) : q0;
+// Four codes as the number c0 + 16 c1 + 256 c2 + 4096 c3 + base in bits 0-15 of the result.  The product with a
+// reciprocal is within 2^-20 of the quotient, so *near is set where that could decide the rounding
+// (then exact_codes4 gives the answer); s = 0 comes with inv = 0 and gives codes 0.
+IFQ_DEVINL uint32_t fast_codes4(const float4& x, float m, float inv, float lo, float hi, float base, bool* near) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, half-even
+  float sum = base;
+  const float* f = &x.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float r = fminf(fmaxf((f[j] - m) * inv, lo), hi);
+    const float n = (r + kMagic) - kMagic;
+    *near |= fabsf(r - n) > 0.49999f;
+    sum = fmaf(n, (float)(1 << (4 * j)), sum);
+  }
+  return __float_as_uint(sum + 8388608.0f) & 0xFFFFu;
+}
+static __device__ __noinline__ uint32_t exact_codes4(float4 x, float s, float m, float lo, float hi, float base) {
+  const float* f = &x.x;
+  float sum = base;
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j)
+    sum += s > 0.0f ? exact_code(f[j], s, m, lo, hi) * (float)(1 << (4 * j)) : 0.0f;
+  return (uint32_t)sum;
+}
+// A group's reciprocal for fast_codes4 (0 where s = 0), and whether it is usable (not for scales so small
+// that it overflows).
+IFQ_DEVINL float code_reciprocal(float s, bool* usable) {
+  *usable = s == 0.0f || s >= 1e-30f;
+  return s >= 1e-30f ? __frcp_rn(s) : 0.0f;
 }
 
 IFQ_DEVINL float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

@@ -51,68 +51,78 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
   const int64_t cu = T.cols / U, local = unit - T.unit_begin;
   const int64_t rt = local / cu, c0 = (local % cu) * U;
 
-  float v[2][C][8];
-  bool bad = false;
+  float4 v[2][C][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t r = rt * 16 + g + 8 * h;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-      if (r < T.rows) {
-        const float4* src = reinterpret_cast<const float4*>(T.R + r * T.cols + c0 + 32 * c + 8 * t);
-        a = __ldcs(src);
-        b = __ldcs(src + 1);
-      }
-      v[h][c][0] = a.x; v[h][c][1] = a.y; v[h][c][2] = a.z; v[h][c][3] = a.w;
-      v[h][c][4] = b.x; v[h][c][5] = b.y; v[h][c][6] = b.z; v[h][c][7] = b.w;
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (!(fabsf(v[h][c][j]) <= 3.402823466e38f)) {
-          v[h][c][j] = 0.0f;
-          bad = true;
-        }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, IFQ_DEV_NONFINITE);
+      for (int i = 0; i < 2; ++i)
+        v[h][c][i] = r < T.rows ? __ldcs(reinterpret_cast<const float4*>(T.R + r * T.cols + c0 + 32 * c + 8 * t) + i)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 
+  bool bad = false;
   uint32_t words[2][C];
 #pragma unroll
   for (int c0g = 0; c0g < C; c0g += kPer) {
     uint32_t sbits[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float m = 0.0f;
+      // odd becomes NaN with a NaN or Inf weight, which the maximum alone would not show
+      auto largest = [&](float* odd) {
+        float m = 0.0f;
 #pragma unroll
-      for (int c = c0g; c < c0g + kPer; ++c)
+        for (int c = c0g; c < c0g + kPer; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[h][c][j]));
+          for (int i = 0; i < 2; ++i) {
+            const float4& x = v[h][c][i];
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+            *odd = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, fmaf(x.w, 0.0f, *odd))));
+          }
+        return m;
+      };
+      float odd = 0.0f, m = largest(&odd);
+      if (!(odd == 0.0f)) {
+        bad = true;
+#pragma unroll
+        for (int c = c0g; c < c0g + kPer; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float* f = &v[h][c][i].x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = fabsf(f[j]) <= 3.402823466e38f ? f[j] : 0.0f;
+          }
+        m = largest(&odd);
+      }
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(m, 1.0f / 7.0f));
       sbits[h] = __bfloat16_as_ushort(sb);
       const float s = __bfloat162float(sb);
-      const float inv = s >= 1e-30f ? __frcp_rn(s) : 0.0f;
+      bool fast;
+      const float inv = code_reciprocal(s, &fast);
+      constexpr float kBase = 8.0f * (1 + 16 + 256 + 4096);  // codes are stored plus 8
 #pragma unroll
       for (int c = c0g; c < c0g + kPer; ++c) {
-        uint32_t n[8];
+        const float4 &a = v[h][c][0], &b = v[h][c][1];
+        uint32_t half[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float q = 0.0f;
-          if (s > 0.0f) q = fminf(fmaxf(q4_round_quotient(v[h][c][j], s, inv), -7.0f), 7.0f);
-          n[j] = (uint32_t)((int)q + 8);
+        for (int i = 0; i < 2; ++i) {  // columns 0, 2, 4, 6 of the word, then 1, 3, 5, 7
+          const float4 x = i == 0 ? make_float4(a.x, a.z, b.x, b.z) : make_float4(a.y, a.w, b.y, b.w);
+          bool near = !fast;
+          half[i] = fast_codes4(x, 0.0f, inv, -7.0f, 7.0f, kBase, &near);
+          if (near) half[i] = exact_codes4(x, s, 0.0f, -7.0f, 7.0f, kBase);
         }
-        words[h][c] = q4_pack_word(n);
+        words[h][c] = half[0] | (half[1] << 16);
       }
     }
     if (t == 0)
       reinterpret_cast<uint32_t*>(T.scales)[(rt * (T.cols / G) + (c0 + 32 * c0g) / G) * 8 + g] =
           sbits[0] | (sbits[1] << 16);
   }
+  if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
 #pragma unroll
   for (int k = 0; k < C / 2; ++k) {
     uint4 w = make_uint4(words[0][2 * k], words[1][2 * k], words[0][2 * k + 1], words[1][2 * k + 1]);
