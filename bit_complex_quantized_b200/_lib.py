@@ -392,12 +392,12 @@ def _enqueue(index, stream, fn, *args):
 
 def _plane(t, numel, dtypes, index, what):
     """Address of a contiguous tensor of `numel` elements and one of the types on CUDA device `index`."""
-    if t.numel() != numel or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{what}: needs a contiguous {dtypes[0]} tensor of {numel} elements, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if t.numel() == numel and t.dtype in dtypes and t.is_contiguous() and t.get_device() == index >= 0:
+        return t.data_ptr()
     if t.get_device() != index or index < 0:
         raise ValueError(f"{what}: all tensors of a call must be on one CUDA device, got {t.device}")
-    return t.data_ptr()
+    raise ValueError(f"{what}: needs a contiguous {dtypes[0]} tensor of {numel} elements, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()}")
 
 
 def _words(words):
@@ -454,17 +454,16 @@ def _w4_layers(layers, group, B):
     """(device index, descriptor words) of ifq_w4_gemv's layers."""
     index, words = layers[0]["codes"].get_device(), []
     for d in layers:
-        rows, cols = d["rows"], d["cols"]
-        c, s = _w4_buffers(d["codes"], d["scales"], rows, cols, group, index)
-        x_im, y_im = d.get("x_im"), d.get("y_im")
+        rows, cols, codes, scales = d["rows"], d["cols"], d["codes"], d["scales"]
+        x_re, x_im, y_re, y_im = d["x_re"], d.get("x_im"), d["y_re"], d.get("y_im")
+        c, s = _w4_buffers(codes, scales, rows, cols, group, index)
         if y_im is not None and rows % 2:
             raise ValueError("planar outputs need an even number of rows")
         xs = B * (cols if x_im is None else cols // 2)
         ys = B * (rows if y_im is None else rows // 2)
-        words += (c, s, rows, cols, _plane(d["x_re"], xs, _BF16, index, "x_re"),
+        words += (c, s, rows, cols, _plane(x_re, xs, _BF16, index, "x_re"),
                   0 if x_im is None else _plane(x_im, xs, _BF16, index, "x_im"),
-                  _plane(d["y_re"], ys, _F32, index, "y_re"),
-                  0 if y_im is None else _plane(y_im, ys, _F32, index, "y_im"))
+                  _plane(y_re, ys, _F32, index, "y_re"), 0 if y_im is None else _plane(y_im, ys, _F32, index, "y_im"))
     return index, _words(words)
 
 
@@ -524,7 +523,14 @@ class Kv4Cache:
 
 def _row_planes(cache, planes, width, dtypes, what):
     """Addresses and the common row stride of [rows][width] planes whose rows may be slices of wider ones."""
-    rows, index, ld = cache.rows, cache.index, None
+    rows, index = cache.rows, cache.index
+    numel = rows * width
+    for t in planes:
+        if not (t.numel() == numel and t.dtype in dtypes and t.is_contiguous() and t.get_device() == index):
+            break
+    else:
+        return [t.data_ptr() for t in planes], width
+    ld = None
     for t in planes:
         if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or t.dtype not in dtypes or t.stride(1) != 1:
             raise ValueError(f"{what}: needs {dtypes[0]} planes [{rows}][{width}], rows contiguous; got {t.dtype} "
