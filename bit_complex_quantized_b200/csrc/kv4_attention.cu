@@ -249,10 +249,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT)) kv4_attn_kerne
       v[j] *= p.scale2;
       mx = fmaxf(mx, fabsf(v[j]));
     }
-    if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // mx < 2^(e + 1); a zero or subnormal row keeps the smallest exponent, an infinite one becomes NaN below
+    if (mx > 0x1p100f) {  // its scores would overflow: the row counts as not finite
+      bad = true;
+      v[0] = NAN;
+    }
+    if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
+    // mx < 2^(e + 1); a zero or tiny row keeps the smallest exponent
     const int e = max((__float_as_int(mx) >> 23) - 127, -100);
     const float f = pow2(14 - e);
 #pragma unroll
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT)) kv4_attn_kerne
     const int row = NT * t + j;
     qs2[j][0] = qsum[row][0];
     qs2[j][1] = qsum[row][1];
-    cs[j] = pow2(min(qexp[row], 117) + 10);  // undoes the 2^-24 of the codes and the row's 2^(14 - e)
+    cs[j] = pow2(min(qexp[row], 100) + 10);  // undoes the 2^-24 of the codes and the row's 2^(14 - e)
     visible[j] = row < nrows ? sq.len - sq.n_new + (qt * QR + row) / p.shared + 1 : 0;
   }
   // keys below this are seen by every row of the tile (rows past the last count as seeing all)
@@ -623,8 +627,11 @@ Plan plan(const ifq_kv4_cache& c, int shared) {
   const int64_t most = (c.table_cols * c.page_tokens + kWarps * kUnit - 1) / (kWarps * kUnit);
   int64_t s = slots / ctas;
   if (c.B > 1 && s < 4) s = 4;
-  if (s > most) s = most;
-  if (s <= kMaxCluster) s = s >= 8 ? 8 : s >= 4 ? 4 : s >= 2 ? 2 : 1;
+  if (s > most && most > kMaxCluster) s = most;
+  if (s <= kMaxCluster || most <= kMaxCluster) {
+    s = s >= 8 ? 8 : s >= 4 ? 4 : s >= 2 ? 2 : 1;
+    while (s / 2 >= most) s /= 2;
+  }
   r.splits = (int)s;
   r.cluster = s <= kMaxCluster ? (int)s : 1;
   r.by_length = c.B > 1 && c.B <= kThreads && ctas * s > slots;

@@ -395,7 +395,7 @@ cudaError_t launch(const AppendParams& p, bool read, cudaStream_t s) {
   const bool tokens = p.c.n_new < 16;
   // threads of 8 entries, or warps of the records that n_new tokens can touch
   const int64_t blocks = tokens ? ((int64_t)p.c.n_new * p.c.kv_heads * (DIM / 2) + kThreads - 1) / kThreads
-                                : ((p.c.n_new + 14) / 16 + 1) * (int64_t)p.c.kv_heads / kWarps + 1;
+                                : (((int64_t)p.c.n_new + 14) / 16 + 1) * p.c.kv_heads / kWarps + 1;
   const dim3 grid((unsigned)blocks, (unsigned)p.c.B);
   if (tokens && read) kv4_read_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
   else if (tokens) kv4_append_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);

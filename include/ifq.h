@@ -522,7 +522,8 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *               n_new rows each.  rows: allocated rows of those buffers; rows that
  *               belong to no sequence are neither read nor written.
  *   pages 1..2^31-1     page_tokens  a multiple of 16, 16..65536
- *   kv_heads 1..1024    B 1..65535    n_new >= 1    table_cols 1..2^26
+ *   kv_heads 1..1024    B 1..65535    n_new >= 1    table_cols 1..2^26, at most
+ *   2^31 - 65536 positions (table_cols * page_tokens)    rows 1..2^31-1
  * page_table, kv_lens and new_offsets are device memory, read when the call's
  * work runs (so a captured graph serves growing lengths).  What they name is checked
  * there: a sequence whose offsets decrease, leave 0..rows or give more
@@ -546,8 +547,9 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *                    terms (2^-22 of the row's largest entry), the weights times a value's scale as one
  *                    (2^-11 relative); sums and the softmax's maximum and sum are float32, and
  *                    stay finite for stored values up to 2^100; partial results are joined in a
- *                    fixed order (bit-reproducible).  A NaN or Inf in q
- *                    sets IFQ_DEV_NONFINITE and makes that row NaN.
+ *                    fixed order (bit-reproducible).  A NaN or Inf in q,
+ *                    or an entry with |scale q| above 2^99, sets IFQ_DEV_NONFINITE and makes
+ *                    that row NaN.
  *   workspace        device scratch of ifq_kv4_attention_workspace_bytes() bytes,
  *                    16-byte aligned, no initial contents needed; calls that share it
  *                    must not overlap on the GPU.  May be NULL when that is 0.

@@ -81,7 +81,7 @@ def _attend(c, heads=8, q=FAKE, o=FAKE, ldq=512, ldo=512, ws=FAKE, nb=1 << 40):
     (dict(records=None), NULL), (dict(page_table=None), NULL), (dict(kv_lens=None), NULL), (dict(pages=0), SHAPE),
     (dict(pages=1 << 31), SHAPE), (dict(page_tokens=8), SHAPE), (dict(page_tokens=24), SHAPE),
     (dict(page_tokens=1 << 17), SHAPE), (dict(kv_heads=0), SHAPE), (dict(dim=48), SHAPE), (dict(dim=256), SHAPE),
-    (dict(B=0), SHAPE), (dict(B=65536, rows=65536), SHAPE), (dict(n_new=0), BATCH), (dict(rows=2), SHAPE),
+    (dict(B=0), SHAPE), (dict(B=65536, rows=65536), SHAPE), (dict(n_new=0), BATCH), (dict(n_new=2), SHAPE), (dict(rows=2), SHAPE),
     (dict(rows=0), SHAPE), (dict(table_cols=0), SHAPE), (dict(table_cols=1 << 26, page_tokens=65536), SHAPE),
     (dict(records=FAKE + 8), ALIGN), (dict(kv_lens=FAKE + 2), ALIGN), (dict(new_offsets=FAKE + 1), ALIGN)])
 def test_cache_argument_errors(kw, status):

@@ -75,7 +75,7 @@ class Case:
         r = self.rng
         self.records[:] = r.integers(0, 256, self.records.shape, dtype=np.uint8)
         par = self.records[..., 32 * self.dim:]
-        s = F.bf16_bits((r.random(par.shape[:-1] + (64,)) * 0.3 * spread + 0.02).astype(np.float32))
+        s = F.bf16_bits(((r.random(par.shape[:-1] + (64,)) * 0.3 + 0.02) * spread).astype(np.float32))
         m = F.bf16_bits((-r.random(par.shape[:-1] + (64,)) * 3 * spread).astype(np.float32))
         par[:] = np.stack([s, m], axis=-1).reshape(par.shape[:-1] + (128,)).view(np.uint8)
         self.d_records.copy_(to_dev(self.records))
@@ -220,6 +220,83 @@ def test_attention_long_and_split():
     c.attention(8)
     torch.cuda.synchronize()
     c.check(8)
+
+
+@pytest.mark.parametrize("B,shared,dim", [(128, 6, 64), (129, 1, 64), (200, 8, 32), (100, 5, 128)])
+def test_attention_many_sequences(B, shared, dim):
+    """More CTAs than the GPU holds: one long sequence (many records a warp, its page numbers fetched 32 at a time)
+    among short and empty ones, wherever it stands in the batch."""
+    lens, news = [1 + b % 3 for b in range(B)], [1] * B
+    lens[B // 2], lens[3], news[3], lens[5] = 20003, 0, 0, 777
+    c = Case(lens, news, 4, dim, 16 if B == 129 else 64, seed=B)
+    c.fill_random()
+    c.attention(shared)
+    torch.cuda.synchronize()
+    c.lens = lens
+    first = [x.clone() for x in c.o]
+    c.check(shared)
+    c.attention(shared, q=c.q)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, c.o))
+
+
+def test_attention_replayed_while_lengths_grow():
+    """A captured call over more splits than a cluster holds, replayed with longer sequences; a second cache's call
+    runs at the same time on another stream with a workspace of its own."""
+    c, other = Case([5000, 9], [1, 1], 1, 64, 64, seed=20, extra_cols=40), Case([3000], [1], 2, 64, 32, seed=21)
+    c.fill_random()
+    other.fill_random()
+    spare = sorted(set(range(c.records.shape[0])) - set(c.table[c.table >= 0].tolist()))
+    assert len(spare) == 2
+    cols = (c.table[0] >= 0).sum()
+    c.table[0, cols], c.d_table[0, cols] = spare[0], spare[0]
+    c.attention(8)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.ifq_kv4_attention(c.cache, *c.d_q, *c.o, scale=c.scale, workspace=c.ws)
+    side = torch.cuda.Stream()
+    for step in range(3):
+        c.lens = [5000 + 7 * step, 9 + step]
+        c.d_lens.copy_(torch.tensor(c.lens, dtype=torch.int32))
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        other.attention(3, stream=side, q=getattr(other, "q", None))
+        torch.cuda.synchronize()
+        c.check(8)
+        other.check(3)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
+def test_attention_scales(scale):
+    c = Case([70, 33], [1, 2], 2, 32, 16, seed=22)
+    c.fill_random()
+    c.attention(2, scale=scale)
+    torch.cuda.synchronize()
+    c.check(2)
+
+
+@pytest.mark.parametrize("spread", [2.0 ** -60, 2.0 ** 60])
+def test_attention_value_range(spread):
+    """Stored values far from 1 (keys too: q is scaled against them)."""
+    c = Case([300], [1], 2, 64, 16, seed=23)
+    c.fill_random(spread)
+    c.attention(2, q_scale=1.0 / spread)
+    torch.cuda.synchronize()
+    c.check(2)
+
+
+def test_attention_huge_query_counts_as_not_finite():
+    c = Case([100, 90], [1, 1], 1, 64, 16, seed=24)
+    c.fill_random()
+    q = [np.random.default_rng(i).standard_normal((c.rows, 64)).astype(np.float32) for i in range(2)]
+    q[1][0, 3] = 3e38
+    st = status_word()
+    c.attention(1, q=q, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.IFQ_DEV_NONFINITE
+    assert torch.isnan(c.o[0][0]).all() and torch.isnan(c.o[1][0]).all()
+    c.check(1, skip=(0,))
 
 
 def test_attention_ignores_what_lies_behind():
