@@ -10,6 +10,7 @@ from ._lib import (  # noqa: F401
     IFQ_DEV_NONFINITE,
     IFQ_DEV_RANGE,
     IFQ_DEV_TIMEOUT,
+    IFQ_KV4_MAX_APPEND,
     IFQ_KV4_MAX_NEW,
     IFQ_MAX_GEMV_BATCH,
     IFQ_MAX_GROUP,

@@ -22,6 +22,7 @@ IFQ_DEV_NONFINITE = 0x1
 IFQ_DEV_TIMEOUT = 0x2
 IFQ_DEV_RANGE = 0x4
 IFQ_KV4_MAX_NEW = 16
+IFQ_KV4_MAX_APPEND = 1048544
 
 EXPORTED = (
     "ifq_status_string",

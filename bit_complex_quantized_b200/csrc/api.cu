@@ -385,7 +385,7 @@ ifq_status check_kv4_rows(const ifq_kv4_cache* c, const void* a, const void* b, 
   if (st != IFQ_OK) return st;
   if (!a || !b || !d || !e) return IFQ_ERR_NULL;
   if (ld < (int64_t)c->kv_heads * c->dim || ld % 4 || ld > (int64_t)1 << 30) return IFQ_ERR_SHAPE;
-  if ((int64_t)c->n_new * c->kv_heads * c->dim > (int64_t)1 << 38) return IFQ_ERR_SHAPE;
+  if (c->n_new > IFQ_KV4_MAX_APPEND) return IFQ_ERR_BATCH;  // a sequence's records are one grid dimension
   if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned16(e)) return IFQ_ERR_ALIGN;
   return check_device();
 }

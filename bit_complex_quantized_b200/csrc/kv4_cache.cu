@@ -7,7 +7,7 @@
 //
 // Two forms.  Fewer than 16 new tokens a sequence (decode): a thread takes 8 entries of a token, dim / 8
 // neighbouring threads a plane, and writes its words and half words alone: as many threads as there are entries, the
-// shortest chain.  More (prompts): a warp takes one record (16 tokens of a head): keys as lane (g, t) holds them in the record (8 entries
+// shortest chain.  More (prompts): a warp takes one plane of one record (16 tokens of a head): keys as lane (g, t) holds them in the record (8 entries
 // of the tokens g and g + 8 per 32 columns), values likewise (4 entries of four tokens), so that loads
 // are 128-byte runs, a plane's minimum and maximum take two or three shuffles, and a record that is
 // all new leaves as 512-byte stores.  A record that holds older tokens too is written token by token: a token's keys
@@ -40,29 +40,26 @@ struct Item {
   int head;
 };
 
-IFQ_DEVINL bool find_item(const AppendParams& p, Item* it) {
-  const Kv4Arg& c = p.c;
-  const int b = blockIdx.y;
-  it->q = kv4_seq(c, b);
-  if (!it->q.ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
-  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  it->head = (int)(item % c.kv_heads);
+// Record `tile` (counted from the first that the new tokens touch) of head `head` of sequence blockIdx.z.
+IFQ_DEVINL bool find_item(const AppendParams& p, const Kv4Seq& q, int32_t tile, int head, Item* it) {
+  it->q = q;
+  it->head = head;
   // a sequence whose length is unusable has no positions, but its rows still read as 0
-  const int32_t len = it->q.ok ? it->q.len : it->q.n_new;
-  it->first = len - it->q.n_new;
-  const int64_t tile = (it->first >> 4) + item / c.kv_heads;
-  if (tile * 16 >= len) return false;
-  it->pos0 = (int32_t)tile * 16;
+  const int32_t len = q.ok ? q.len : q.n_new;
+  it->first = len - q.n_new;
+  tile += it->first >> 4;
+  if ((int64_t)tile * 16 >= len) return false;
+  it->pos0 = tile * 16;
   it->rec = nullptr;
-  if (it->q.ok) {
-    it->rec = kv4_record(c, b, it->head, (int32_t)tile);
+  if (q.ok) {
+    it->rec = kv4_record(p.c, blockIdx.z, head, tile);
     if (!it->rec && (threadIdx.x & 31) == 0) set_status(p.status, IFQ_DEV_RANGE);
   }
   return true;
 }
 
 struct Group {  // a plane's parameters
-  float s, m, inv;
+  float s, m, factor;
   uint32_t bits;
   bool fast;
 };
@@ -72,14 +69,14 @@ IFQ_DEVINL Group group_of(float lo, float hi) {
   Group r;
   r.s = __bfloat162float(sb);
   r.m = __bfloat162float(mb);
-  r.inv = code_reciprocal(r.s, &r.fast);
+  r.factor = code_factor(r.s, 1.0f / 15.0f, &r.fast);
   r.bits = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
   return r;
 }
 // Entry j of four in bits 4 j.
 IFQ_DEVINL uint32_t codes_of(const float4& x, const Group& q) {
   bool near = !q.fast;
-  const uint32_t w = fast_codes4(x, q.m, q.inv, 0.0f, 15.0f, 0.0f, &near);
+  const uint32_t w = fast_codes4<15>(make_float4(x.x - q.m, x.y - q.m, x.z - q.m, x.w - q.m), q.factor, 0.0f, 0.0f, &near);
   return near ? exact_codes4(x, q.s, q.m, 0.0f, 15.0f, 0.0f) : w;
 }
 // The word of eight entries of a key: entries 0, 2, 4, 6 in the low half, 1, 3, 5, 7 in the high half.
@@ -169,31 +166,31 @@ __global__ void __launch_bounds__(kThreads) kv4_append_tokens_kernel(const __gri
   if (part == 0) *reinterpret_cast<uint32_t*>(rec + 16 * D + (plane >> 1) * 128 + r * 8 + (plane & 1) * 4) = gq.bits;
 }
 
+// One plane of a record's keys (planes 0, 1) or values (2, 3): warp w of the CTA takes plane w.
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int D = 2 * DIM, CH = D / 32, CP = DIM / 32;
+  constexpr int D = 2 * DIM, CP = DIM / 32;
+  static_assert(kWarps == 4, "a warp per plane");
+  const Kv4Seq seq = kv4_seq(p.c, blockIdx.z);
+  if (!seq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   Item it;
-  if (!find_item(p, &it) || !it.rec) return;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (!find_item(p, seq, blockIdx.y, blockIdx.x, &it) || !it.rec) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, plane = threadIdx.x >> 5, pl = plane & 1;
   const int32_t len = it.q.len;
   auto in = [&](int r) { return it.pos0 + r >= it.first && it.pos0 + r < len; };
-  auto row = [&](const float* base, int r) {
-    return base + (it.q.row0 + it.pos0 + r - it.first) * p.ld + it.head * DIM;
-  };
+  const float* src = p.src[plane] + (it.q.row0 + it.pos0 - it.first) * p.ld + it.head * DIM;
   const bool all = in(0) && in(15);
   bool bad = false;
-  uint32_t* par = reinterpret_cast<uint32_t*>(it.rec + 16 * D);
-
-  uint32_t words[CH][2];  // {32-column chunk, token g or g + 8}
-#pragma unroll
-  for (int pl = 0; pl < 2; ++pl) {
+  uint32_t* par = reinterpret_cast<uint32_t*>(it.rec + 16 * D) + (plane >> 1) * 32 + pl;
+  uint32_t words[CP][2];  // {32-column chunk of the plane, h}
+  if (plane < 2) {        // keys: tokens g + 8 h, entries 8 t .. 8 t + 7 of a chunk
     float4 v[2][CP][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int c = 0; c < CP; ++c)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) v[h][c][i] = take(row(p.src[pl], g + 8 * h) + c * 32 + t * 8 + i * 4, in(g + 8 * h));
+        for (int i = 0; i < 2; ++i) v[h][c][i] = take(src + (g + 8 * h) * p.ld + c * 32 + t * 8 + i * 4, in(g + 8 * h));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
@@ -218,26 +215,11 @@ __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __gr
       }
       const Group q = group_of(lo, hi);
 #pragma unroll
-      for (int c = 0; c < CP; ++c) words[pl * CP + c][h] = key_word(v[h][c][0], v[h][c][1], q);
-      if (t == 0 && in(g + 8 * h)) par[(g + 8 * h) * 2 + pl] = q.bits;
+      for (int c = 0; c < CP; ++c) words[c][h] = key_word(v[h][c][0], v[h][c][1], q);
+      if (t == 0 && in(g + 8 * h)) par[(g + 8 * h) * 2] = q.bits;
     }
-  }
-#pragma unroll
-  for (int k = 0; k < CH / 2; ++k) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(it.rec + k * 512 + lane * 16);
-    if (all) {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(words[2 * k][0], words[2 * k][1], words[2 * k + 1][0], words[2 * k + 1][1]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (in(g + 8 * (e & 1))) dst[e] = words[2 * k + (e >> 1)][e & 1];
-    }
-  }
-
-  // values: {32-column chunk, tokens 2 t + 8 h and 2 t + 8 h + 1}
-#pragma unroll
-  for (int pl = 0; pl < 2; ++pl) {
-    float4 v[2][2][CP];  // {h, token of the pair, chunk}: entries 4 g .. 4 g + 3
+  } else {                // values: tokens 2 t + 8 h + e, entries 4 g .. 4 g + 3 of a chunk
+    float4 v[2][2][CP];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -245,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __gr
 #pragma unroll
         for (int c = 0; c < CP; ++c) {
           const int r = 2 * t + 8 * h + e;
-          v[h][e][c] = take(row(p.src[2 + pl], r) + c * 32 + g * 4, in(r));
+          v[h][e][c] = take(src + r * p.ld + c * 32 + g * 4, in(r));
         }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -272,21 +254,29 @@ __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __gr
 #pragma unroll
         for (int c = 0; c < CP; ++c) {
           const uint32_t w = codes_of(v[h][e][c], q) << (16 * e);
-          words[pl * CP + c][h] = e == 0 ? w : words[pl * CP + c][h] | w;
+          words[c][h] = e == 0 ? w : words[c][h] | w;
         }
-        if (g == 0 && in(r)) par[32 + r * 2 + pl] = q.bits;
+        if (g == 0 && in(r)) par[r * 2] = q.bits;
       }
   }
 #pragma unroll
-  for (int k = 0; k < CH / 2; ++k) {
-    uint8_t* dst = it.rec + 8 * D + k * 512 + lane * 16;
-    if (all) {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(words[2 * k][0], words[2 * k][1], words[2 * k + 1][0], words[2 * k + 1][1]);
+  for (int c = 0; c < CP; ++c) {  // chunk ch is the words 2 (ch % 2) + h of the 16 bytes of its pair of chunks
+    const int ch = pl * CP + c;
+    uint8_t* dst = it.rec + (plane >> 1) * 8 * D + (ch >> 1) * 512 + lane * 16 + (ch & 1) * 8;
+    if (all && CP > 1) {
+      if (c & 1)
+        *reinterpret_cast<uint4*>(dst - 8) = make_uint4(words[c - (CP > 1)][0], words[c - (CP > 1)][1], words[c][0], words[c][1]);
+    } else if (all) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(words[c][0], words[c][1]);
+    } else if (plane < 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (in(g + 8 * h)) reinterpret_cast<uint32_t*>(dst)[h] = words[c][h];
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)  // half words: token 2 t + 8 h + (e & 1)
-        if (in(2 * t + 8 * ((e >> 1) & 1) + (e & 1)))
-          reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(words[2 * k + (e >> 2)][(e >> 1) & 1] >> (16 * (e & 1)));
+      for (int e = 0; e < 4; ++e)  // half words: token 2 t + 8 h + (e & 1)
+        if (in(2 * t + 8 * (e >> 1) + (e & 1)))
+          reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(words[c][e >> 1] >> (16 * (e & 1)));
     }
   }
   if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
@@ -295,8 +285,11 @@ __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __gr
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv4_read_records_kernel(const __grid_constant__ AppendParams p) {
   constexpr int D = 2 * DIM, CH = D / 32, CP = DIM / 32;
+  const Kv4Seq seq = kv4_seq(p.c, blockIdx.z);
+  if (!seq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
+  const int head = blockIdx.x * kWarps + (threadIdx.x >> 5);
   Item it;
-  if (!find_item(p, &it)) return;
+  if (head >= p.c.kv_heads || !find_item(p, seq, blockIdx.y, head, &it)) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int32_t end = it.first + it.q.n_new;
   auto in = [&](int r) { return it.pos0 + r >= it.first && it.pos0 + r < end; };
@@ -393,14 +386,18 @@ __global__ void __launch_bounds__(kThreads) kv4_read_tokens_kernel(const __grid_
 template <int DIM>
 cudaError_t launch(const AppendParams& p, bool read, cudaStream_t s) {
   const bool tokens = p.c.n_new < 16;
-  // threads of 8 entries, or warps of the records that n_new tokens can touch
-  const int64_t blocks = tokens ? ((int64_t)p.c.n_new * p.c.kv_heads * (DIM / 2) + kThreads - 1) / kThreads
-                                : (((int64_t)p.c.n_new + 14) / 16 + 1) * p.c.kv_heads / kWarps + 1;
-  const dim3 grid((unsigned)blocks, (unsigned)p.c.B);
-  if (tokens && read) kv4_read_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
-  else if (tokens) kv4_append_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
-  else if (read) kv4_read_records_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
-  else kv4_append_records_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+  if (tokens) {  // threads of 8 entries
+    const int64_t blocks = ((int64_t)p.c.n_new * p.c.kv_heads * (DIM / 2) + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)blocks, (unsigned)p.c.B);
+    if (read) kv4_read_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+    else kv4_append_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+  } else {       // the records that n_new tokens can touch, a CTA (appending) or a warp each; heads fastest, so that
+                 // CTAs that run together read neighbouring columns
+    const unsigned tiles = (unsigned)(((int64_t)p.c.n_new + 14) / 16 + 1);
+    const unsigned heads = (unsigned)p.c.kv_heads;
+    if (read) kv4_read_records_kernel<DIM><<<dim3((heads + kWarps - 1) / kWarps, tiles, p.c.B), kThreads, 0, s>>>(p);
+    else kv4_append_records_kernel<DIM><<<dim3(heads, tiles, p.c.B), kThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 

@@ -76,22 +76,24 @@ IFQ_DEVINL float exact_code(float x, float s, float m, float lo, float hi) {
   return fminf(fmaxf(n, lo), hi);
 }
 
-// Four codes as the number c0 + 16 c1 + 256 c2 + 4096 c3 + base in bits 0-15 of the result.  The product with a
-// reciprocal is within 2^-20 of the quotient, so *near is set where that could decide the rounding
-// (then exact_codes4 gives the answer); s = 0 comes with inv = 0 and gives codes 0.
-IFQ_DEVINL uint32_t fast_codes4(const float4& x, float m, float inv, float lo, float hi, float base, bool* near) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, half-even
+// Four codes n_j = rint(kSpan r_j), r = a d + bias saturated to [0, 1], as the number n0 + 16 n1 + 256 n2 + 4096 n3 +
+// base in bits 0-15 of the result.  kSpan r is within 2^-18 of the quotient that it stands for, so *near is set
+// where that could decide the rounding (then exact_codes4 gives the answer).
+template <int kSpan>
+IFQ_DEVINL uint32_t fast_codes4(const float4& d, float a, float bias, float base, bool* near) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer
   float sum = base;
-  const float* f = &x.x;
+  const float* f = &d.x;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float r = fminf(fmaxf((f[j] - m) * inv, lo), hi);
-    const float n = (r + kMagic) - kMagic;
-    *near |= fabsf(r - n) > 0.49999f;
+    const float r = __saturatef(fmaf(f[j], a, bias));
+    const float n = fmaf(r, (float)kSpan, kMagic) - kMagic;
+    *near |= fabsf(fmaf(r, (float)kSpan, -n)) > 0.49999f;
     sum = fmaf(n, (float)(1 << (4 * j)), sum);
   }
   return __float_as_uint(sum + 8388608.0f) & 0xFFFFu;
 }
+// The same by exact_code, code + base per entry; codes 0 where s = 0.
 static __device__ __noinline__ uint32_t exact_codes4(float4 x, float s, float m, float lo, float hi, float base) {
   const float* f = &x.x;
   float sum = base;
@@ -100,11 +102,11 @@ static __device__ __noinline__ uint32_t exact_codes4(float4 x, float s, float m,
     sum += s > 0.0f ? exact_code(f[j], s, m, lo, hi) * (float)(1 << (4 * j)) : 0.0f;
   return (uint32_t)sum;
 }
-// A group's reciprocal for fast_codes4 (0 where s = 0), and whether it is usable (not for scales so small
-// that it overflows).
-IFQ_DEVINL float code_reciprocal(float s, bool* usable) {
+// A group's factor 1 / (span s) for fast_codes4 (0 where s = 0), and whether it is usable (not for scales so
+// small that it overflows).
+IFQ_DEVINL float code_factor(float s, float inv_span, bool* usable) {
   *usable = s == 0.0f || s >= 1e-30f;
-  return s >= 1e-30f ? __frcp_rn(s) : 0.0f;
+  return s >= 1e-30f ? __frcp_rn(s) * inv_span : 0.0f;
 }
 
 IFQ_DEVINL float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

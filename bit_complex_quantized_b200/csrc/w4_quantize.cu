@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
       sbits[h] = __bfloat16_as_ushort(sb);
       const float s = __bfloat162float(sb);
       bool fast;
-      const float inv = code_reciprocal(s, &fast);
-      constexpr float kBase = 8.0f * (1 + 16 + 256 + 4096);  // codes are stored plus 8
+      const float factor = code_factor(s, 1.0f / 14.0f, &fast);
+      constexpr float kOnes = 1 + 16 + 256 + 4096;  // codes are stored plus 8; q + 7 = 14 (w / (14 s) + 1/2)
 #pragma unroll
       for (int c = c0g; c < c0g + kPer; ++c) {
         const float4 &a = v[h][c][0], &b = v[h][c][1];
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
         for (int i = 0; i < 2; ++i) {  // columns 0, 2, 4, 6 of the word, then 1, 3, 5, 7
           const float4 x = i == 0 ? make_float4(a.x, a.z, b.x, b.z) : make_float4(a.y, a.w, b.y, b.w);
           bool near = !fast;
-          half[i] = fast_codes4(x, 0.0f, inv, -7.0f, 7.0f, kBase, &near);
-          if (near) half[i] = exact_codes4(x, s, 0.0f, -7.0f, 7.0f, kBase);
+          half[i] = fast_codes4<14>(x, factor, 0.5f, kOnes, &near);
+          if (near) half[i] = exact_codes4(x, s, 0.0f, -7.0f, 7.0f, 8.0f * kOnes);
         }
         words[h][c] = half[0] | (half[1] << 16);
       }

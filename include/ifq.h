@@ -535,7 +535,8 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  * appends to must not be shared.
  *
  * ifq_kv4_append     k_re, k_im, v_re, v_im [rows][kv_heads dim] float32, rows ld
- *                    elements apart: quantized into the records.  Any n_new.
+ *                    elements apart: quantized into the records.  n_new <=
+ *                    IFQ_KV4_MAX_APPEND.
  * ifq_kv4_read       the stored values of the same tokens, as float32 (s n + m
  *                    rounded once): what attention uses.
  * ifq_kv4_attention  q_re, q_im [rows][q_heads dim] float32, rows ldq apart, head h
@@ -558,6 +559,7 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  * n_new outside its range is IFQ_ERR_BATCH.  dev_status may be NULL.
  * ------------------------------------------------------------------------- */
 #define IFQ_KV4_MAX_NEW 16
+#define IFQ_KV4_MAX_APPEND 1048544
 
 typedef struct {
   uint8_t* records;

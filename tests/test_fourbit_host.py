@@ -104,6 +104,7 @@ def test_cache_call_errors():
     assert _attend(c, heads=0) == SHAPE and _attend(c, heads=2) == SHAPE and _attend(c, heads=9) == SHAPE
     assert _attend(c, heads=4100) == SHAPE
     assert _attend(_cache(n_new=17, rows=51)) == BATCH
+    assert _append(_cache(n_new=Q.IFQ_KV4_MAX_APPEND + 1, new_offsets=FAKE)) == BATCH
     assert _attend(c, q=None) == NULL and _attend(c, o=None) == NULL
     assert _attend(c, q=FAKE + 4) == ALIGN and _attend(c, o=FAKE + 2) == ALIGN
     assert _attend(c, ldq=508) == SHAPE and _attend(c, ldq=514) == SHAPE and _attend(c, ldo=513) == SHAPE
