@@ -994,6 +994,45 @@ def run_case(args):
         def fn():
             Q.ifq_dequantize([(cb, sc, outp[0], outp[1])], 2)
         label = "dequantize bf16 llama7b gate T=2"
+    elif args.case == "w4":
+        # the workload's layers kept in 4 bits (groups of 128), --batch tokens, one call
+        cfg = W.config(args.workload)
+        layers, nbytes = [], 0
+        for i, spec in enumerate(cfg.layers):
+            rows, cols = spec.real_shape
+            cs, ss = Q.w4_shapes(rows, cols, 128)
+            xr, xi = W.activations(cfg, i, args.batch)
+            layers.append(dict(codes=torch.randint(0, 256, cs, dtype=torch.uint8, device=dev, generator=g),
+                               scales=torch.full(ss, 0.01, dtype=torch.bfloat16, device=dev), rows=rows, cols=cols,
+                               x_re=xr.to(dev), x_im=xi.to(dev), y_re=torch.empty((args.batch, spec.N), device=dev),
+                               y_im=torch.empty((args.batch, spec.N), device=dev)))
+            nbytes += rows * cols // 2 + rows * cols // 64 + args.batch * (2 * cols + 4 * rows)
+        wset = Q.W4LayerSet(layers, 128, args.batch)
+
+        def fn():
+            Q.ifq_w4_gemv(wset, 128, args.batch)
+        label = f"4-bit gemv {args.workload} B={args.batch}"
+    elif args.case == "kv4":
+        # one decode step of --batch sequences of 8192 tokens on the 4-bit cache: 8 key/value heads of 64 complex
+        # entries, 64 query heads (llama70b) or 32 heads (llama7b); append, then attention
+        H, q_heads = (8, 64) if args.workload == "llama70b" else (32, 32)
+        length, page, dim, B = 8192, 64, 64, args.batch
+        per = length // page
+        rec = torch.randint(0, 256, Q.Kv4Cache.records_shape(B * per, H, page, dim), dtype=torch.uint8, device=dev,
+                            generator=g)
+        rec[..., 32 * dim:].view(torch.bfloat16)[:] = 0.1
+        table = torch.randperm(B * per, device=dev, generator=g).to(torch.int32).view(B, per)
+        cache = Q.Kv4Cache(rec, table, torch.full((B,), length, dtype=torch.int32, device=dev), dim)
+        kv = [torch.randn((B, H * dim), device=dev, generator=g) for _ in range(4)]
+        q = [torch.randn((B, q_heads * dim), device=dev, generator=g) for _ in range(2)]
+        o = [torch.empty((B, q_heads * dim), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+        wsb = torch.empty(max(16, Q.ifq_kv4_attention_workspace_bytes(cache, q_heads)), dtype=torch.uint8, device=dev)
+        nbytes = B * (length * H * (2 * dim + 16) + H * dim * 16 + q_heads * dim * 12)
+
+        def fn():
+            Q.ifq_kv4_append(cache, *kv)
+            Q.ifq_kv4_attention(cache, *q, *o, scale=(2 * dim) ** -0.5, workspace=wsb)
+        label = f"4-bit cache step {args.workload} B={B}, {length} tokens"
     elif args.case == "convert":
         cfg = W.config("llama7b")
         spec = cfg.layers[4]
@@ -1031,7 +1070,7 @@ def main():
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--impl", choices=["ours", "reference"], default="ours")
-    ap.add_argument("--case", choices=["gemv", "gemm", "quant", "convert", "wlq", "dequant"], default=None)
+    ap.add_argument("--case", choices=["gemv", "gemm", "quant", "convert", "wlq", "dequant", "w4", "kv4"], default=None)
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--workload", choices=["llama7b", "llama70b"], default="llama70b", help="layer set of --case gemv")
     ap.add_argument("--cpu-seconds", type=float, default=12.0)

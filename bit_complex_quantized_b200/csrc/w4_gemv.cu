@@ -5,8 +5,8 @@
 // (q4_common.cuh), x is the B operand as it is, so all products are exact and a group accumulates
 // in float32; the group's scale multiplies that sum in float32.
 //
-// HBM-bound by the codes.  A CTA of 4 warps takes 128 rows x a slice of the columns; its warps take
-// the slice's 64-column tiles in turn, each for all 128 rows, so that a tile's x is read from
+// HBM-bound by the codes.  A CTA of 4 warps takes 64 rows x a slice of the columns; its warps take
+// 128-column stages of the slice in turn, each for all 64 rows, so that a tile's x is read from
 // shared memory once for all strips, nothing is shared between warps, and the loop has no
 // barrier: every warp runs its own ring of asynchronous copies (codes, scales, x of one tile a stage).
 // The warps' sums are added in shared memory at the end, and where a layer has few row tiles its
@@ -20,8 +20,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStrips = 4;                 // 16-row strips of a CTA
-constexpr int kRows = kStrips * 16;
+constexpr int kStrips = 4;                 // 16-row strips of a warp
 constexpr int kCols = 128;                 // of a stage: two tiles
 constexpr int kSplits = 4;                 // a layer's columns are split over 1, 2, 4 or 8 CTAs
 
@@ -45,20 +44,27 @@ struct LParams {
   uint32_t* status;
 };
 
-// A warp's stage: two 64-column tiles of all strips, their scales and the x of up to XB tokens.
+// A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 8 tokens the x of a
+// stage is as large as a warp's codes, so two warps with different rows take the same columns and share it (half
+// the copies of x: 72 us against 74.6 us for the 70B-shaped gate and down layers at 16 tokens).
 template <int G, int XB>
 struct Ring {
   static constexpr int NT = (XB + 7) / 8;
+  static constexpr int kRowWarps = XB > 8 ? 2 : 1;                      // warps with the same columns
+  static constexpr int kColWarps = kWarps / kRowWarps;
+  static constexpr int kRows = kRowWarps * kStrips * 16;                // of a CTA
   static constexpr int kStripBytes = 2 * kQ4TileBytes;
   static constexpr int kScaleBytes = kCols / G * 32;                    // of a strip
   static constexpr int kCodes = kStrips * kStripBytes;
   static constexpr int kScales = kStrips * kScaleBytes;
   static constexpr int kX = XB * kCols * 2;
-  static constexpr int kStage = kCodes + kScales + kX;
+  static constexpr int kStage = kCodes + kScales;
   static constexpr int kStages = 2;
-  static constexpr int kBytes = kWarps * kStages * kStage;
-  static constexpr int kCtas = 227 * 1024 / (kBytes + 1024);            // that an SM holds
-  static_assert(kBytes >= kWarps * kRows * XB * 4, "the sums reuse the ring");
+  static constexpr int kXRing = kWarps * kStages * kStage;              // offset of the x rings
+  static constexpr int kBytes = kXRing + kColWarps * kStages * kX;
+  static constexpr int kCtas = XB > 8 ? 3 : XB > 2 ? 4 : 5;             // that an SM holds: the registers are cut to this
+  static_assert(kCtas * (kBytes + 1024) <= 227 * 1024, "shared memory of an SM");
+  static_assert(kBytes >= kColWarps * kRows * XB * 4, "the sums reuse the ring");
 };
 
 IFQ_DEVINL uint32_t cluster_rank() {
@@ -78,9 +84,9 @@ IFQ_DEVINL float ld_cluster(const void* smem, uint32_t rank) {
 }
 
 template <int G, int XB, int kCap>
-__global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant__ LParams<kCap> p) {
+__global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas)) w4_gemv_kernel(const __grid_constant__ LParams<kCap> p) {
   using R = Ring<G, XB>;
-  constexpr int NT = R::NT;
+  constexpr int NT = R::NT, kRows = R::kRows, kColWarps = R::kColWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
   const int cl = (int)blockIdx.x / p.cluster;
@@ -88,33 +94,35 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
   while (li + 1 < p.count && cl >= p.l[li + 1].cluster_begin) ++li;
   const LArg& L = p.l[li];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // this CTA's rows, and its columns [kb, ke) in whole stages; this warp's stages are warp, + kWarps, ...
+  // this CTA's rows, and its columns [kb, ke) in whole stages; this warp's stages are col_warp, + kColWarps, ...
   const int sub = rank % L.split;
   const int tile = (cl - L.cluster_begin) * (p.cluster / L.split) + rank / L.split;
   const int64_t row0 = (int64_t)tile * kRows;
   const int units = (L.cols + kCols - 1) / kCols, per = (units + L.split - 1) / L.split;
   const int kb = min(units, sub * per) * kCols, ke = tile < L.tiles ? min(L.cols, kb + per * kCols) : kb;
-  const int k_first = kb + warp * kCols;
+  const int row_warp = warp % R::kRowWarps, col_warp = warp / R::kRowWarps;
+  const int k_first = kb + col_warp * kCols;
 
   // Sources of this lane's copies, moved on to the warp's next stage after each.  Strips past the layer repeat its
   // last one.
-  const int64_t strips = (L.rows + 15) / 16;
+  const int64_t strips = (L.rows + 15) / 16, strip0 = row0 / 16 + row_warp * kStrips;
   const uint8_t* code_src[kStrips];
 #pragma unroll
   for (int m = 0; m < kStrips; ++m)
-    code_src[m] = L.codes + min(strips - 1, row0 / 16 + m) * (L.cols * 8ll) + k_first * 8ll + lane * 16;
+    code_src[m] = L.codes + min(strips - 1, strip0 + m) * (L.cols * 8ll) + k_first * 8ll + lane * 16;
   constexpr int kLanes = R::kScaleBytes / 16;                 // lanes that fetch a strip's scales
   const uint8_t* scale_src = reinterpret_cast<const uint8_t*>(L.scales) +
-                             min(strips - 1, row0 / 16 + lane / kLanes) * (L.cols / G * 32ll) + k_first / G * 32 +
+                             min(strips - 1, strip0 + lane / kLanes) * (L.cols / G * 32ll) + k_first / G * 32 +
                              (lane % kLanes) * 16;
-  const int xt = lane >> 4, xv = lane & 15;                   // 8 columns of the tokens xt + 2 i
+  constexpr int kXTokens = 2 * R::kRowWarps;                  // tokens that the warps of a column fetch at a time
+  const int xt = (lane >> 4) + 2 * row_warp, xv = lane & 15;  // 8 columns of the tokens xt + kXTokens i
   int xk = k_first + xv * 8;
   bool second = xk >= L.x_split;
   const uint16_t* x_src = second ? L.x[1] + xt * (L.cols - L.x_split) + (xk - L.x_split) : L.x[0] + xt * L.x_split + xk;
-  int64_t x_step = 2 * (second ? L.cols - L.x_split : L.x_split);
+  int64_t x_step = kXTokens * (second ? L.cols - L.x_split : L.x_split);
   const uint32_t ring = smem_u32(smem) + warp * R::kStages * R::kStage;
   const uint32_t code_dst = ring + lane * 16, scale_dst = ring + R::kCodes + lane * 16;
-  const uint32_t x_dst = ring + R::kCodes + R::kScales + ((xv >> 2) * XB * 4 + (xv & 3)) * 16 + xt * 64;
+  const uint32_t x_dst = smem_u32(smem) + R::kXRing + col_warp * R::kStages * R::kX + ((xv >> 2) * XB * 4 + (xv & 3)) * 16 + xt * 64;
   int kl = k_first;   // columns of the next load
   auto load = [&](int slot) {
     if (kl < ke) {
@@ -123,27 +131,27 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
       for (int m = 0; m < kStrips; ++m) {
         cp_async16(code_dst + slot * R::kStage + m * R::kStripBytes, code_src[m]);
         if (whole) cp_async16(code_dst + slot * R::kStage + m * R::kStripBytes + kQ4TileBytes, code_src[m] + kQ4TileBytes);
-        code_src[m] += kWarps * R::kStripBytes;
+        code_src[m] += kColWarps * R::kStripBytes;
       }
       if (lane < kStrips * kLanes && (whole || (lane % kLanes) * 16 < 64 / G * 32))
         cp_async16(scale_dst + slot * R::kStage, scale_src);
-      scale_src += kWarps * R::kScaleBytes;
+      scale_src += kColWarps * R::kScaleBytes;
       if (xk < ke) {
         const uint16_t* src = x_src;
 #pragma unroll
-        for (int i = 0; i < (XB + 1) / 2; ++i) {
-          if (2 * i >= p.B) break;
-          if (xt + 2 * i < p.B) cp_async16(x_dst + slot * R::kStage + i * 128, src);
+        for (int i = 0; i < (XB + kXTokens - 1) / kXTokens; ++i) {
+          if (kXTokens * i >= p.B) break;
+          if (xt + kXTokens * i < p.B) cp_async16(x_dst + slot * R::kX + i * kXTokens * 64, src);
           src += x_step;
         }
       }
-      kl += kWarps * kCols;
-      xk += kWarps * kCols;
-      x_src += kWarps * kCols;
+      kl += kColWarps * kCols;
+      xk += kColWarps * kCols;
+      x_src += kColWarps * kCols;
       if (!second && xk >= L.x_split) {
         second = true;
         x_src = L.x[1] + xt * (L.cols - L.x_split) + (xk - L.x_split);
-        x_step = 2 * (L.cols - L.x_split);
+        x_step = kXTokens * (L.cols - L.x_split);
       }
     }
     cp_async_commit();
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
   const uint8_t* xs[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
-    xs[nt] = base0 + R::kCodes + R::kScales + (min(nt * 8 + g, p.B - 1) * 4 + t) * 16;
+    xs[nt] = smem + R::kXRing + col_warp * R::kStages * R::kX + (min(nt * 8 + g, p.B - 1) * 4 + t) * 16;
 
   auto tile_product = [&](int slot, int i) {
     uint4 b[2][NT];
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        b[c][nt] = *reinterpret_cast<const uint4*>(xs[nt] + slot * R::kStage + (2 * i + c) * XB * 64);
+        b[c][nt] = *reinterpret_cast<const uint4*>(xs[nt] + slot * R::kX + (2 * i + c) * XB * 64);
 #pragma unroll
     for (int m = 0; m < kStrips; ++m) {
       const uint4 w4 = *reinterpret_cast<const uint4*>(base0 + lane * 16 + slot * R::kStage + m * R::kStripBytes +
@@ -203,10 +211,12 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
   for (int st = 0; st < R::kStages - 1; ++st) load(st);
   for (int k = k_first; k < ke;) {
 #pragma unroll
-    for (int slot = 0; slot < R::kStages; ++slot, k += kWarps * kCols) {
+    for (int slot = 0; slot < R::kStages; ++slot, k += kColWarps * kCols) {
       if (k >= ke) break;
       cp_async_wait<R::kStages - 2>();
-      __syncwarp();  // every lane's copies of the stage are in, and the previous stage has been read
+      // every lane's copies of the stage are in, and the previous stage has been read
+      if constexpr (R::kRowWarps == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + col_warp), "n"(32 * R::kRowWarps) : "memory");
       load((slot + R::kStages - 1) % R::kStages);
       tile_product(slot, 0);
       if (k + kCols <= ke) tile_product(slot, 1);
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
   cp_async_wait<0>();
   __syncthreads();
 
-  // sums[warp][n][row] in the ring's memory; added over the warps, then over the cluster
+  // sums[col_warp][n][row] in the ring's memory; added over the columns' warps, then over the cluster
   float* sums = reinterpret_cast<float*>(smem);
   const int plane = p.B * kRows;
 #pragma unroll
@@ -225,12 +235,15 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int n = nt * 8 + 2 * t + (e & 1);
-        if (n < p.B) sums[warp * plane + n * kRows + m * 16 + g + 8 * (e >> 1)] = acc[m][nt][e];
+        if (n < p.B) sums[col_warp * plane + n * kRows + (row_warp * kStrips + m) * 16 + g + 8 * (e >> 1)] = acc[m][nt][e];
       }
   __syncthreads();
+  auto column_sum = [&](const float* at) {
+    if constexpr (kColWarps == 2) return at[0] + at[plane];
+    else return (at[0] + at[plane]) + (at[2 * plane] + at[3 * plane]);
+  };
   if (p.cluster > 1) {
-    for (int i = threadIdx.x; i < plane; i += kThreads)
-      sums[i] = (sums[i] + sums[plane + i]) + (sums[2 * plane + i] + sums[3 * plane + i]);
+    for (int i = threadIdx.x; i < plane; i += kThreads) sums[i] = column_sum(sums + i);
     cluster_sync();
   }
   bool bad = false;
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) w4_gemv_kernel(const __grid_constant
       v = 0.0f;
       for (int k = 0; k < L.split; ++k) v += ld_cluster(at, rank - sub + k);
     } else {
-      v = p.cluster > 1 ? at[0] : (at[0] + at[plane]) + (at[2 * plane] + at[3 * plane]);
+      v = p.cluster > 1 ? at[0] : column_sum(at);
     }
     v *= kQ4Unit;
     bad |= !(fabsf(v) <= 3.402823466e38f);
@@ -279,8 +292,8 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
   int64_t stages[kCap][kSplits], tiles[kCap], longest = 0;
   for (int i = 0; i < count; ++i) {
     const int64_t units = (Ls[i].cols + kCols - 1) / kCols;
-    for (int k = 0; k < kSplits; ++k) stages[i][k] = (units + (kWarps << k) - 1) / (kWarps << k);
-    tiles[i] = (Ls[i].rows + kRows - 1) / kRows;
+    for (int k = 0; k < kSplits; ++k) stages[i][k] = (units + (R::kColWarps << k) - 1) / (R::kColWarps << k);
+    tiles[i] = (Ls[i].rows + R::kRows - 1) / R::kRows;
     longest = stages[i][0] > longest ? stages[i][0] : longest;
   }
   auto split_for = [&](int i, int64_t len) {

@@ -27,21 +27,24 @@ struct QArg {
   int64_t unit_begin;  // first unit (16 rows x U columns) of the tensor in the call
 };
 
+// Capacity kCap >= count: a launch copies its parameters, and most calls have few tensors.
+template <int kCap>
 struct QParams {
-  QArg t[IFQ_MAX_GROUP];
+  QArg t[kCap];
   int count;
   int64_t units;
   uint32_t* status;
 };
 
-__device__ __forceinline__ int find_tensor(const QParams& p, int64_t unit) {
+template <int kCap>
+__device__ __forceinline__ int find_tensor(const QParams<kCap>& p, int64_t unit) {
   int i = 0;
   while (i + 1 < p.count && unit >= p.t[i + 1].unit_begin) ++i;
   return i;
 }
 
-template <int G>
-__global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constant__ QParams p) {
+template <int G, int kCap>
+__global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constant__ QParams<kCap> p) {
   constexpr int U = G > 64 ? G : 64, C = U / 32;      // columns and 32-column chunks of a unit
   constexpr int kPer = G / 32;                        // chunks of a group
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -130,8 +133,8 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
   }
 }
 
-template <int G>
-__global__ void __launch_bounds__(kThreads) w4_dequant_kernel(const __grid_constant__ QParams p) {
+template <int G, int kCap>
+__global__ void __launch_bounds__(kThreads) w4_dequant_kernel(const __grid_constant__ QParams<kCap> p) {
   constexpr int U = G > 64 ? G : 64;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= p.units) return;
@@ -168,17 +171,31 @@ __global__ void __launch_bounds__(kThreads) w4_dequant_kernel(const __grid_const
     }
 }
 
-template <typename Fill>
-void fill(QParams& p, int count, int group, Fill f) {
+enum class Op { kQuantize, kDequantize };
+
+template <Op kOp, int G, int kCap>
+void run(const QParams<kCap>& p, cudaStream_t s) {
+  const unsigned grid = (unsigned)((p.units + kWarps - 1) / kWarps);
+  if constexpr (kOp == Op::kQuantize) w4_quant_kernel<G, kCap><<<grid, kThreads, 0, s>>>(p);
+  else w4_dequant_kernel<G, kCap><<<grid, kThreads, 0, s>>>(p);
+}
+
+// arg(i): the i-th tensor's pointers and sizes.
+template <Op kOp, int kCap, typename Arg>
+cudaError_t launch(int count, int group, uint32_t* dev_status, cudaStream_t s, Arg arg) {
+  QParams<kCap> p;
   p.count = count;
-  const int64_t U = group > 64 ? group : 64;
-  int64_t units = 0;
+  p.status = dev_status;
+  p.units = 0;
   for (int i = 0; i < count; ++i) {
-    f(p.t[i], i);
-    p.t[i].unit_begin = units;
-    units += (p.t[i].rows + 15) / 16 * (p.t[i].cols / U);
+    p.t[i] = arg(i);
+    p.t[i].unit_begin = p.units;
+    p.units += w4_units(p.t[i].rows, p.t[i].cols, group);
   }
-  p.units = units;
+  if (group == 32) run<kOp, 32>(p, s);
+  else if (group == 64) run<kOp, 64>(p, s);
+  else run<kOp, 128>(p, s);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -186,36 +203,18 @@ void fill(QParams& p, int count, int group, Fill f) {
 int64_t w4_units(int64_t rows, int64_t cols, int group) { return (rows + 15) / 16 * (cols / (group > 64 ? group : 64)); }
 
 cudaError_t launch_w4_quantize(const ifq_w4_tensor* ts, int count, int group, uint32_t* dev_status, cudaStream_t s) {
-  QParams p = {};
-  fill(p, count, group, [&](QArg& a, int i) {
-    a.R = ts[i].R;
-    a.codes = ts[i].codes;
-    a.scales = ts[i].scales;
-    a.rows = ts[i].rows;
-    a.cols = ts[i].cols;
-  });
-  p.status = dev_status;
-  const unsigned grid = (unsigned)((p.units + kWarps - 1) / kWarps);
-  if (group == 32) w4_quant_kernel<32><<<grid, kThreads, 0, s>>>(p);
-  else if (group == 64) w4_quant_kernel<64><<<grid, kThreads, 0, s>>>(p);
-  else w4_quant_kernel<128><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  auto arg = [&](int i) { return QArg{ts[i].R, ts[i].codes, ts[i].scales, nullptr, ts[i].rows, ts[i].cols, 0}; };
+  return count <= 8 ? launch<Op::kQuantize, 8>(count, group, dev_status, s, arg)
+                    : launch<Op::kQuantize, IFQ_MAX_GROUP>(count, group, dev_status, s, arg);
 }
 
 cudaError_t launch_w4_dequantize(const ifq_w4_dqtensor* ts, int count, int group, cudaStream_t s) {
-  QParams p = {};
-  fill(p, count, group, [&](QArg& a, int i) {
-    a.codes = const_cast<uint8_t*>(ts[i].codes);
-    a.scales = const_cast<uint16_t*>(ts[i].scales);
-    a.out = ts[i].w;
-    a.rows = ts[i].rows;
-    a.cols = ts[i].cols;
-  });
-  const unsigned grid = (unsigned)((p.units + kWarps - 1) / kWarps);
-  if (group == 32) w4_dequant_kernel<32><<<grid, kThreads, 0, s>>>(p);
-  else if (group == 64) w4_dequant_kernel<64><<<grid, kThreads, 0, s>>>(p);
-  else w4_dequant_kernel<128><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  auto arg = [&](int i) {
+    return QArg{nullptr, const_cast<uint8_t*>(ts[i].codes), const_cast<uint16_t*>(ts[i].scales), ts[i].w, ts[i].rows,
+                ts[i].cols, 0};
+  };
+  return count <= 8 ? launch<Op::kDequantize, 8>(count, group, nullptr, s, arg)
+                    : launch<Op::kDequantize, IFQ_MAX_GROUP>(count, group, nullptr, s, arg);
 }
 
 }  // namespace ifq
