@@ -8,10 +8,16 @@
 // HBM-bound by the codes.  A CTA of 4 warps takes 64 rows x a slice of the columns; its warps take
 // 128-column stages of the slice in turn, each for all 64 rows, so that a tile's x is read from
 // shared memory once for all strips, nothing is shared between warps, and the loop has no
-// barrier: every warp runs its own ring of asynchronous copies (codes, scales, x of one tile a stage).
+// barrier: every warp runs its own ring of asynchronous copies (codes, scales and x of a stage).
 // The warps' sums are added in shared memory at the end, and where a layer has few row tiles its
 // columns are split over a cluster, whose CTAs add theirs through distributed shared memory: one launch,
 // no workspace, a fixed order of sums.
+//
+// Bound: a word takes 5 integer, 4 bf16 and 1 (2 above 8 tokens) matrix instructions and with loads, scales and
+// copies 16 to 20 issue slots, where the copy rate leaves about 22.  7B-shaped block, 1 token (105 MB): 21 us, 5 TB/s,
+// 77 % of the copy rate, the rest start and end.  50021 x 4096 in groups of 32, 5 tokens: 28 us, 65 % (a group costs
+// 7 instructions per 2 words).  70B-shaped gate and down, 16 tokens: 72 us, 54 %, issue-bound at 12 warps an SM
+// (the accumulators and operands of 16 tokens take 143 registers).
 #include "ifq_internal.h"
 #include "q4_common.cuh"
 
@@ -44,8 +50,8 @@ struct LParams {
   uint32_t* status;
 };
 
-// A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 8 tokens the x of a
-// stage is as large as a warp's codes, so two warps with different rows take the same columns and share it (half
+// A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 8 tokens the x of
+// a stage is as large as a warp's codes, so two warps with different rows take the same columns and share it (half
 // the copies of x: 72 us against 74.6 us for the 70B-shaped gate and down layers at 16 tokens).
 template <int G, int XB>
 struct Ring {
@@ -62,7 +68,7 @@ struct Ring {
   static constexpr int kStages = 2;
   static constexpr int kXRing = kWarps * kStages * kStage;              // offset of the x rings
   static constexpr int kBytes = kXRing + kColWarps * kStages * kX;
-  static constexpr int kCtas = XB > 8 ? 3 : XB > 2 ? 4 : 5;             // that an SM holds: the registers are cut to this
+  static constexpr int kCtas = XB > 8 ? 3 : XB > 2 ? 4 : 5;             // that an SM holds (the registers' limit)
   static_assert(kCtas * (kBytes + 1024) <= 227 * 1024, "shared memory of an SM");
   static_assert(kBytes >= kColWarps * kRows * XB * 4, "the sums reuse the ring");
 };
@@ -84,7 +90,8 @@ IFQ_DEVINL float ld_cluster(const void* smem, uint32_t rank) {
 }
 
 template <int G, int XB, int kCap>
-__global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas)) w4_gemv_kernel(const __grid_constant__ LParams<kCap> p) {
+__global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas))
+    w4_gemv_kernel(const __grid_constant__ LParams<kCap> p) {
   using R = Ring<G, XB>;
   constexpr int NT = R::NT, kRows = R::kRows, kColWarps = R::kColWarps;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -122,15 +129,17 @@ __global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas)) w4_gemv_kernel
   int64_t x_step = kXTokens * (second ? L.cols - L.x_split : L.x_split);
   const uint32_t ring = smem_u32(smem) + warp * R::kStages * R::kStage;
   const uint32_t code_dst = ring + lane * 16, scale_dst = ring + R::kCodes + lane * 16;
-  const uint32_t x_dst = smem_u32(smem) + R::kXRing + col_warp * R::kStages * R::kX + ((xv >> 2) * XB * 4 + (xv & 3)) * 16 + xt * 64;
+  const uint32_t x_dst = smem_u32(smem) + R::kXRing + col_warp * R::kStages * R::kX +
+                         ((xv >> 2) * XB * 4 + (xv & 3)) * 16 + xt * 64;
   int kl = k_first;   // columns of the next load
   auto load = [&](int slot) {
     if (kl < ke) {
       const bool whole = kl + kCols <= ke;  // a layer's last stage may be one tile
 #pragma unroll
       for (int m = 0; m < kStrips; ++m) {
-        cp_async16(code_dst + slot * R::kStage + m * R::kStripBytes, code_src[m]);
-        if (whole) cp_async16(code_dst + slot * R::kStage + m * R::kStripBytes + kQ4TileBytes, code_src[m] + kQ4TileBytes);
+        const uint32_t dst = code_dst + slot * R::kStage + m * R::kStripBytes;
+        cp_async16(dst, code_src[m]);
+        if (whole) cp_async16(dst + kQ4TileBytes, code_src[m] + kQ4TileBytes);
         code_src[m] += kColWarps * R::kStripBytes;
       }
       if (lane < kStrips * kLanes && (whole || (lane % kLanes) * 16 < 64 / G * 32))
@@ -235,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas)) w4_gemv_kernel
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int n = nt * 8 + 2 * t + (e & 1);
-        if (n < p.B) sums[col_warp * plane + n * kRows + (row_warp * kStrips + m) * 16 + g + 8 * (e >> 1)] = acc[m][nt][e];
+        const int row = (row_warp * kStrips + m) * 16 + g + 8 * (e >> 1);
+        if (n < p.B) sums[col_warp * plane + n * kRows + row] = acc[m][nt][e];
       }
   __syncthreads();
   auto column_sum = [&](const float* at) {

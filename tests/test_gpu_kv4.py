@@ -240,6 +240,18 @@ def test_attention_many_sequences(B, shared, dim):
     assert all(torch.equal(a, b) for a, b in zip(first, c.o))
 
 
+def test_attention_more_sequences_than_are_counted():
+    """More sequences than the kernel counts by length: a CTA per head and tile of rows."""
+    B = 1100
+    lens, news = [1 + b % 5 for b in range(B)], [1] * B
+    lens[700], lens[9], news[9] = 3000, 0, 0
+    c = Case(lens, news, 1, 32, 16, seed=31)
+    c.fill_random()
+    c.attention(2)
+    torch.cuda.synchronize()
+    c.check(2)
+
+
 def test_attention_replayed_while_lengths_grow():
     """A captured call over more splits than a cluster holds, replayed with longer sequences; a second cache's call
     runs at the same time on another stream with a workspace of its own."""
