@@ -14,10 +14,10 @@
 // no workspace, a fixed order of sums.
 //
 // Bound: a word takes 5 integer, 4 bf16 and 1 (2 above 8 tokens) matrix instructions and with loads, scales and
-// copies 16 to 20 issue slots, where the copy rate leaves about 22.  7B-shaped block, 1 token (105 MB): 21 us, 5 TB/s,
-// 77 % of the copy rate, the rest start and end.  50021 x 4096 in groups of 32, 5 tokens: 28 us, 65 % (a group costs
-// 7 instructions per 2 words).  70B-shaped gate and down, 16 tokens: 72 us, 54 %, issue-bound at 12 warps an SM
-// (the accumulators and operands of 16 tokens take 143 registers).
+// copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 21.3 us,
+// 76 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
+// groups of 32, 5 tokens: 28 us, 65 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us, the
+// layer set 117 us, 59 %: issue at 12 to 16 warps an SM (the accumulators and operands of 16 tokens fill the registers).
 #include "ifq_internal.h"
 #include "q4_common.cuh"
 
@@ -52,7 +52,7 @@ struct LParams {
 
 // A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 8 tokens the x of
 // a stage is as large as a warp's codes, so two warps with different rows take the same columns and share it (half
-// the copies of x: 72 us against 74.6 us for the 70B-shaped gate and down layers at 16 tokens).
+// the copies of x: a 7B-shaped block at 16 tokens 41 us, 46 us without).
 template <int G, int XB>
 struct Ring {
   static constexpr int NT = (XB + 7) / 8;
@@ -68,7 +68,10 @@ struct Ring {
   static constexpr int kStages = 2;
   static constexpr int kXRing = kWarps * kStages * kStage;              // offset of the x rings
   static constexpr int kBytes = kXRing + kColWarps * kStages * kX;
-  static constexpr int kCtas = XB > 8 ? 3 : XB > 2 ? 4 : 5;             // that an SM holds (the registers' limit)
+  // CTAs that an SM holds, which the registers are cut to.  Above 8 tokens: 4 (128 registers: 117 us for a 70B-shaped
+  // layer set at 16 tokens, 135 us with 3), but 3 for groups of 32, whose scales take more (162 registers: 50021 x 4096
+  // at 16 tokens 37 us, 40 us with 4).
+  static constexpr int kCtas = XB > 8 ? (G == 32 ? 3 : 4) : XB > 2 ? 4 : 5;
   static_assert(kCtas * (kBytes + 1024) <= 227 * 1024, "shared memory of an SM");
   static_assert(kBytes >= kColWarps * kRows * XB * 4, "the sums reuse the ring");
 };
@@ -291,6 +294,45 @@ cudaError_t allow_smem(K kernel, int bytes, uint64_t* done) {
   return e;
 }
 
+// When the CTAs of a launch end: the places on the GPU by the time at which each is free.
+struct Ends {
+  static constexpr int kMax = 24;
+  int64_t at[kMax], places[kMax];
+  int n = 1;
+  explicit Ends(int64_t all) : at{0}, places{all} {}
+  // `count` CTAs that take `time` each go to the places that are free first.
+  void run(int64_t count, int64_t time) {
+    while (count > 0) {
+      int first = 0;
+      int64_t all = 0;
+      for (int i = 0; i < n; ++i) {
+        if (at[i] < at[first]) first = i;
+        all += places[i];
+      }
+      if (count >= 4 * all || n == kMax) {  // whole rounds of many CTAs
+        const int64_t rounds = count / all > 1 ? count / all : 1;
+        for (int i = 0; i < n; ++i) at[i] += rounds * time;
+        count -= rounds * all;
+        continue;
+      }
+      const int64_t m = count < places[first] ? count : places[first];
+      if (m == places[first]) {
+        at[first] += time;
+      } else {
+        places[first] -= m;
+        at[n] = at[first] + time;
+        places[n++] = m;
+      }
+      count -= m;
+    }
+  }
+  int64_t last() const {
+    int64_t t = 0;
+    for (int i = 0; i < n; ++i) t = at[i] > t ? at[i] : t;
+    return t;
+  }
+};
+
 template <int G, int XB, int kCap>
 cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_status, cudaStream_t s) {
   using R = Ring<G, XB>;
@@ -306,33 +348,42 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
     tiles[i] = (Ls[i].rows + R::kRows - 1) / R::kRows;
     longest = stages[i][0] > longest ? stages[i][0] : longest;
   }
+  // How far to split the columns: to slices of at most `len` stages.  Splitting further helps while CTAs are few or long
+  // ones end last, and costs every CTA its start and join (kStart stages' time): of the lengths that some layer can be
+  // cut to, the one whose CTAs, started longest first on the GPU's places, end first.
+  constexpr int kStart = 6;
   auto split_for = [&](int i, int64_t len) {
     int k = 0;
     while (k + 1 < kSplits && stages[i][k] > len) ++k;
     return k;
   };
-  // How far to split the columns.  Halving the longest slice helps while CTAs are few or long ones end last, and
-  // costs each CTA its start and join (kStart stages' time): the least of (work per slot) + (longest slice) / 2.
-  constexpr int kStart = 6;
-  int best = 0;
-  int64_t best_cost = 0;
-  for (int q = 0; q < kSplits; ++q) {
-    const int64_t len = (longest + (1 << q) - 1) >> q;
-    int64_t work = 0, top = 0;
-    for (int i = 0; i < count; ++i) {
-      const int k = split_for(i, len);
-      work += (tiles[i] << k) * (stages[i][k] + kStart);
-      top = stages[i][k] > top ? stages[i][k] : top;
+  int64_t best = longest, best_end = 0;
+  for (int c = 0; c < count * kSplits; ++c) {
+    const int64_t len = stages[c / kSplits][c % kSplits];
+    bool seen = false;
+    for (int e = 0; e < c && !seen; ++e) seen = stages[e / kSplits][e % kSplits] == len;
+    if (seen) continue;
+    Ends ends(148 * R::kCtas);
+    for (int64_t top = longest + 1;;) {  // the CTAs of each length, longest first
+      int64_t next = 0, n = 0;
+      for (int i = 0; i < count; ++i) {
+        const int k = split_for(i, len);
+        const int64_t st = stages[i][k];
+        if (st < top && st > next) next = st, n = 0;
+        if (st == next) n += tiles[i] << k;
+      }
+      if (next == 0) break;
+      ends.run(n, next + kStart);
+      top = next;
     }
-    const int64_t cost = 2 * work / (148 * R::kCtas) + top;
-    if (q == 0 || cost < best_cost) {
-      best = q;
-      best_cost = cost;
+    if (best_end == 0 || ends.last() < best_end) {
+      best = len;
+      best_end = ends.last();
     }
   }
   int split[kCap], cluster = 1;
   for (int i = 0; i < count; ++i) {
-    split[i] = split_for(i, (longest + (1 << best) - 1) >> best);
+    split[i] = split_for(i, best);
     cluster = (1 << split[i]) > cluster ? 1 << split[i] : cluster;
   }
   // the longest slices first, so that the last CTAs to start are short ones
