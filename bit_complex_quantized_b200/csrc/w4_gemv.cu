@@ -16,8 +16,9 @@
 // Bound: a word takes 5 integer, 4 bf16 and 1 (2 above 8 tokens) matrix instructions and with loads, scales and
 // copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 21.3 us,
 // 76 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
-// groups of 32, 5 tokens: 28 us, 65 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us, the
-// layer set 117 us, 59 %: issue at 12 to 16 warps an SM (the accumulators and operands of 16 tokens fill the registers).
+// groups of 32, 5 tokens: 28 us, 65 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
+// the layer set 117 us, 59 %: issue at 12 to 16 warps an SM (the accumulators and operands of 16 tokens fill the
+// registers).
 #include "ifq_internal.h"
 #include "q4_common.cuh"
 
@@ -52,7 +53,8 @@ struct LParams {
 
 // A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 8 tokens the x of
 // a stage is as large as a warp's codes, so two warps with different rows take the same columns and share it (half
-// the copies of x: a 7B-shaped block at 16 tokens 41 us, 46 us without).
+// the copies of x, and room for a fourth CTA: 72 us against 74.6 us for the 70B-shaped gate and down layers at 16
+// tokens, with three).
 template <int G, int XB>
 struct Ring {
   static constexpr int NT = (XB + 7) / 8;
@@ -348,9 +350,9 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
     tiles[i] = (Ls[i].rows + R::kRows - 1) / R::kRows;
     longest = stages[i][0] > longest ? stages[i][0] : longest;
   }
-  // How far to split the columns: to slices of at most `len` stages.  Splitting further helps while CTAs are few or long
-  // ones end last, and costs every CTA its start and join (kStart stages' time): of the lengths that some layer can be
-  // cut to, the one whose CTAs, started longest first on the GPU's places, end first.
+  // How far to split the columns: to slices of at most `len` stages.  Splitting further helps while CTAs are few or
+  // long ones end last, and costs every CTA its start and join (kStart stages' time): of the lengths that some layer
+  // can be cut to, the one whose CTAs, started longest first on the GPU's places, end first.
   constexpr int kStart = 6;
   auto split_for = [&](int i, int64_t len) {
     int k = 0;
