@@ -430,9 +430,15 @@ def _w4_buffers(codes, scales, rows, cols, group, index):
             _plane(scales, entries // group, _BF16, index, "scales"))
 
 
+def _some(items):
+    if not items:
+        _check(9)  # IFQ_ERR_COUNT
+    return items
+
+
 def ifq_w4_quantize(tensors, group, dev_status=None, stream=None):
     """tensors: list of (R float32 [rows][cols], codes uint8, scales bf16), the last two written, of w4_shapes()."""
-    index, words = tensors[0][0].get_device(), []
+    index, words = _some(tensors)[0][0].get_device(), []
     for R, codes, scales in tensors:
         rows, cols = R.shape
         c, s = _w4_buffers(codes, scales, rows, cols, group, index)
@@ -443,7 +449,7 @@ def ifq_w4_quantize(tensors, group, dev_status=None, stream=None):
 
 def ifq_w4_dequantize(tensors, group, stream=None):
     """tensors: list of (codes, scales, w bf16 [rows][cols]), w written."""
-    index, words = tensors[0][0].get_device(), []
+    index, words = _some(tensors)[0][0].get_device(), []
     for codes, scales, w in tensors:
         rows, cols = w.shape
         c, s = _w4_buffers(codes, scales, rows, cols, group, index)
@@ -453,7 +459,7 @@ def ifq_w4_dequantize(tensors, group, stream=None):
 
 def _w4_layers(layers, group, B):
     """(device index, descriptor words) of ifq_w4_gemv's layers."""
-    index, words = layers[0]["codes"].get_device(), []
+    index, words = _some(layers)[0]["codes"].get_device(), []
     for d in layers:
         rows, cols, codes, scales = d["rows"], d["cols"], d["codes"], d["scales"]
         x_re, x_im, y_re, y_im = d["x_re"], d.get("x_im"), d["y_re"], d.get("y_im")

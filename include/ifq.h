@@ -519,7 +519,8 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  * new tokens    a sequence's new tokens are its last ones, and consecutive rows
  *               of q, k, v and o: rows new_offsets[b] .. new_offsets[b+1] - 1
  *               (int32 [B+1], at most n_new each), or with new_offsets NULL
- *               n_new rows each.  rows: allocated rows of those buffers; rows that
+ *               n_new rows each (launches are sized by n_new: give the most that a
+ *               sequence has, not more).  rows: allocated rows of those buffers; rows that
  *               belong to no sequence are neither read nor written.
  *   pages 1..2^31-1     page_tokens  a multiple of 16, 16..65536
  *   kv_heads 1..1024    B 1..65535    n_new >= 1    table_cols 1..2^26, at most

@@ -129,6 +129,11 @@ def test_python_refuses_wrong_tensors():
         Q.ifq_w4_quantize([(R[:, ::2], codes, scales)], 64)
     with pytest.raises(ValueError):
         Q.ifq_w4_quantize([(R, codes, scales)], 48)
+    for call in (Q.ifq_w4_quantize, Q.ifq_w4_dequantize):
+        with pytest.raises(Q.IfqError):
+            call([], 64)
+    with pytest.raises(Q.IfqError):
+        Q.ifq_w4_gemv([], 64, 1)
     with pytest.raises(ValueError):
         Q.Kv4Cache(torch.zeros(2, 1, 1, 100, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.int32),
                    torch.zeros(1, dtype=torch.int32), 64)

@@ -388,6 +388,42 @@ def test_attention_bad_numbers_in_device_memory():
     c.check(2)
 
 
+def test_bad_numbers_among_many_sequences():
+    """The same checks where the work is counted over the batch: bad lengths, offsets and pages change nothing for
+    the others, and every bad kind is reported."""
+    B, heads, shared = 160, 4, 8
+    rng = np.random.default_rng(40)
+    lens = [int(n) for n in rng.integers(1, 400, B)]
+    news = [int(min(n, 1 + i % 3)) for i, n in enumerate(lens)]
+    c = Case(lens, news, heads, 64, 32, seed=40, n_new=3)
+    c.fill_random()
+    bad_len, empty, bad_page = 17, 60, 101
+    d_lens, table = c.d_lens.clone(), c.d_table.clone()
+    d_lens[bad_len] = 10 ** 7
+    d_lens[empty] = -5
+    table[bad_page] = c.records.shape[0]
+    c.cache = Q.Kv4Cache(c.d_records, table, d_lens, 64, n_new=3, rows=c.rows, new_offsets=c.d_offs)
+    st = status_word()
+    c.attention(shared, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.IFQ_DEV_RANGE
+    c.check(shared, skip=(bad_len, empty, bad_page))
+    for b in (bad_len, empty, bad_page):
+        for x in c.o:
+            assert torch.all(x[c.offs[b]:c.offs[b + 1]] == 0)
+    offs = c.d_offs.clone()
+    offs[50], offs[90] = c.rows + 7, -3              # two sequences each lose their rows
+    c.cache = Q.Kv4Cache(c.d_records, c.d_table, c.d_lens, 64, n_new=3, rows=c.rows, new_offsets=offs)
+    st.zero_()
+    c.attention(shared, q=c.q, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.IFQ_DEV_RANGE
+    c.check(shared, skip=(49, 50, 89, 90))
+    for b in (49, 50, 89, 90):                       # never written
+        for x in c.o:
+            assert torch.all(x[c.offs[b]:c.offs[b + 1]] == 77.0)
+
+
 def test_attention_nonfinite_query_stays_in_its_row():
     c = Case([100, 90], [1, 1], 1, 64, 16, seed=11)
     c.fill_random()

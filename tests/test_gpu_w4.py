@@ -217,3 +217,33 @@ def test_gemv_block_graph_and_stream():
     for d, W, x in made:
         xv = torch.cat([d["x_re"], d["x_im"]], dim=1).float().cpu().numpy().astype(np.float64)
         check_layer(d, W, xv, group)
+
+
+def test_gemv_two_calls_at_once():
+    """Two calls on two streams share nothing: both give what they give alone."""
+    rng = np.random.default_rng(8)
+    a, Wa, xa = make_layer(2048, 2048, 128, 2, True, True, rng)
+    b, Wb, xb = make_layer(1500, 4096, 128, 11, False, False, rng)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        Q.ifq_w4_gemv([a], 128, 2)
+        Q.ifq_w4_gemv([b], 128, 11, stream=side)
+    torch.cuda.synchronize()
+    check_layer(a, Wa, xa, 128)
+    check_layer(b, Wb, xb, 128)
+
+
+def test_gemv_layer_set_repeats_the_call():
+    rng = np.random.default_rng(9)
+    made = [make_layer(r, 512, 64, 3, True, True, rng) for r in (64, 200, 1024)]
+    layers = Q.W4LayerSet([m[0] for m in made], 64, 3)
+    for _ in range(2):
+        for d, _, _ in made:
+            d["y_re"].fill_(-1.0)
+        Q.ifq_w4_gemv(layers, 64, 3)
+        torch.cuda.synchronize()
+        for d, W, x in made:
+            check_layer(d, W, x, 64)
+    with pytest.raises(ValueError):
+        Q.ifq_w4_gemv(layers, 64, 2)
