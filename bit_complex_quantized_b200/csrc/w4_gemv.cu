@@ -7,8 +7,8 @@
 //
 // HBM-bound by the codes.  A CTA of 4 warps takes 64 rows x a slice of the columns; its warps take
 // 128-column stages of the slice in turn, each for all 64 rows, so that a tile's x is read from
-// shared memory once for all strips, nothing is shared between warps, and the loop has no
-// barrier: every warp runs its own ring of asynchronous copies (codes, scales and x of a stage).
+// shared memory once for all strips, and every warp runs its own ring of asynchronous copies (codes,
+// scales and x of a stage) without a barrier of the CTA.
 // The warps' sums are added in shared memory at the end, and where a layer has few row tiles its
 // columns are split over a cluster, whose CTAs add theirs through distributed shared memory: one launch,
 // no workspace, a fixed order of sums.
@@ -16,7 +16,7 @@
 // Bound: a word takes 5 integer, 4 bf16 and 1 (2 above 8 tokens) matrix instructions and with loads, scales and
 // copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 21.3 us,
 // 76 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
-// groups of 32, 5 tokens: 28 us, 65 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
+// groups of 32, 5 tokens: 26 us, 69 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
 // the layer set 117 us, 59 %: issue at 12 to 16 warps an SM (the accumulators and operands of 16 tokens fill the
 // registers).
 #include "ifq_internal.h"
@@ -51,14 +51,14 @@ struct LParams {
   uint32_t* status;
 };
 
-// A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 8 tokens the x of
-// a stage is as large as a warp's codes, so two warps with different rows take the same columns and share it (half
-// the copies of x, and room for a fourth CTA: 72 us against 74.6 us for the 70B-shaped gate and down layers at 16
-// tokens, with three).
+// A stage: two 64-column tiles of a warp's strips, their scales and the x of up to XB tokens.  Above 4 tokens the x of
+// a stage is half a warp's codes or more, so two warps with different rows take the same columns and share it (half
+// the copies of x: 72 us against 74.6 us for the 70B-shaped gate and down layers at 16 tokens, 54.5 us against 59.1 us
+// at 8).  Up to 4 tokens every warp has its own.
 template <int G, int XB>
 struct Ring {
   static constexpr int NT = (XB + 7) / 8;
-  static constexpr int kRowWarps = XB > 8 ? 2 : 1;                      // warps with the same columns
+  static constexpr int kRowWarps = XB > 4 ? 2 : 1;                      // warps with the same columns
   static constexpr int kColWarps = kWarps / kRowWarps;
   static constexpr int kRows = kRowWarps * kStrips * 16;                // of a CTA
   static constexpr int kStripBytes = 2 * kQ4TileBytes;
@@ -72,8 +72,9 @@ struct Ring {
   static constexpr int kBytes = kXRing + kColWarps * kStages * kX;
   // CTAs that an SM holds, which the registers are cut to.  Above 8 tokens: 4 (128 registers: 117 us for a 70B-shaped
   // layer set at 16 tokens, 135 us with 3), but 3 for groups of 32, whose scales take more (162 registers: 50021 x 4096
-  // at 16 tokens 37 us, 40 us with 4).
-  static constexpr int kCtas = XB > 8 ? (G == 32 ? 3 : 4) : XB > 2 ? 4 : 5;
+  // at 16 tokens 37 us, 40 us with 4).  5 to 8: 4 (a 7B-shaped block 29.6 us at 8 tokens, 32.0 us with 5 for groups of
+  // 64 and more).  Up to 4: 5.
+  static constexpr int kCtas = XB > 8 ? (G == 32 ? 3 : 4) : XB > 4 ? 4 : 5;
   static_assert(kCtas * (kBytes + 1024) <= 227 * 1024, "shared memory of an SM");
   static_assert(kBytes >= kColWarps * kRows * XB * 4, "the sums reuse the ring");
 };
@@ -437,6 +438,7 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
 template <int G, int kCap>
 cudaError_t by_batch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_status, cudaStream_t s) {
   if (B <= 2) return launch<G, 2, kCap>(Ls, count, B, dev_status, s);
+  if (B <= 4) return launch<G, 4, kCap>(Ls, count, B, dev_status, s);
   if (B <= 8) return launch<G, 8, kCap>(Ls, count, B, dev_status, s);
   return launch<G, 16, kCap>(Ls, count, B, dev_status, s);
 }

@@ -132,6 +132,23 @@ def test_gemv(rows, cols, group, B, planar):
     check_layer(d, W, x, group)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("count", [1, 9])
+@pytest.mark.parametrize("B", [2, 3, 4, 5, 8, 9])
+def test_gemv_batches(B, count, group):
+    """The last and first batches of each form of the kernel, which differ in the rows of a CTA and in who fetches x;
+    rows around a CTA's 64 and 128."""
+    rng = np.random.default_rng(100 * B + count)
+    made = [make_layer(r, 128 * (3 + i % 3), group, B, False, r % 2 == 0, rng)
+            for i, r in enumerate([65, 64, 128, 129, 127, 63, 192, 193, 16][:count])]
+    st = status_word()
+    Q.ifq_w4_gemv([m[0] for m in made], group, B, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    for m in made:
+        check_layer(*m, group)
+
+
 @pytest.mark.parametrize("B", [1, 7, 16])
 def test_gemv_grouped_layers_and_mixed_planes(B):
     """Layers of one call with different shapes and plane forms; cols 64 (mod 128) splits the planes inside a tile."""
