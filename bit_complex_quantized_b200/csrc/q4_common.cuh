@@ -60,6 +60,8 @@ IFQ_DEVINL void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+constexpr float kWideScale = 1e37f;  // 16 such steps are below the largest float32
+
 // rint((x - m) / s) half-even of the exact quotient, clamped to [lo, hi], for finite x and bf16 values s > 0, m.
 // d + e = x - m (two-term sum); the quotient of d decides except next to a half, where the residual d - s n
 // (exact in float32: both are multiples of one unit and it is at most 1.5 s) plus e is compared with s / 2.
@@ -93,19 +95,27 @@ IFQ_DEVINL uint32_t fast_codes4(const float4& d, float a, float bias, float base
   }
   return __float_as_uint(sum + 8388608.0f) & 0xFFFFu;
 }
-// The same by exact_code, code + base per entry; codes 0 where s = 0.
+// v 2^-8, which keeps the sign of the smallest numbers: of those only the side of a half that they are on matters.
+IFQ_DEVINL float shrink(float v) {
+  const float r = v * 0.00390625f;
+  return r == 0.0f && v != 0.0f ? copysignf(1.401298464e-45f, v) : r;
+}
+// The same by exact_code, code + base per entry; codes 0 where s = 0.  Where s is so large that x - m may overflow,
+// all three are divided by 2^8.
 static __device__ __noinline__ uint32_t exact_codes4(float4 x, float s, float m, float lo, float hi, float base) {
   const float* f = &x.x;
   float sum = base;
+  const bool wide = s > kWideScale;
+  const float ss = wide ? shrink(s) : s, sm = wide ? shrink(m) : m;
 #pragma unroll 1
   for (int j = 0; j < 4; ++j)
-    sum += s > 0.0f ? exact_code(f[j], s, m, lo, hi) * (float)(1 << (4 * j)) : 0.0f;
+    sum += s > 0.0f ? exact_code(wide ? shrink(f[j]) : f[j], ss, sm, lo, hi) * (float)(1 << (4 * j)) : 0.0f;
   return (uint32_t)sum;
 }
 // A group's factor 1 / (span s) for fast_codes4 (0 where s = 0), and whether it is usable (not for scales so
-// small that it overflows).
+// small that it overflows, or so large that x - m may).
 IFQ_DEVINL float code_factor(float s, float inv_span, bool* usable) {
-  *usable = s == 0.0f || s >= 1e-30f;
+  *usable = s == 0.0f || (s >= 1e-30f && s <= kWideScale);
   return s >= 1e-30f ? __frcp_rn(s) * inv_span : 0.0f;
 }
 

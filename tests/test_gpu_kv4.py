@@ -172,6 +172,27 @@ def test_append_range_and_nonfinite():
     np.testing.assert_array_equal(c.d_records.cpu().numpy(), c.records)
 
 
+@pytest.mark.parametrize("new", [3, 16])
+def test_append_widest_groups(new):
+    """Groups whose spread passes float32: x - m overflows where the quotient does not."""
+    c = Case([16], [new], 1, 64, 16, seed=7, fill=0)
+    planes = c.planes()
+    rng = np.random.default_rng(new)
+    big = np.float32(3.38e38)
+    for i, x in enumerate(planes):
+        x[:new] = rng.uniform(-1, 1, (new, 64)).astype(np.float32) * big
+        x[0, :2] = -big, big                               # steps of 2 big / 15: 0 is half way between two of them
+        x[0, 2:8] = 0.0, 1e-45, -1e-45, 1e-30, -1e-30, 1.0
+        x[1, :2] = 1e-45, big                              # one-sided: no overflow, the smallest minimum
+        x[1, 2:] = np.abs(x[1, 2:])
+    st = status_word()
+    Q.ifq_kv4_append(c.cache, *[to_dev(x) for x in planes], dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    c.put(planes)
+    np.testing.assert_array_equal(c.d_records.cpu().numpy(), c.records)
+
+
 def test_append_takes_column_slices():
     """k and v as column slices of one wide output (a fused q, k, v product)."""
     c = Case([5, 9], [2, 1], 2, 64, 16, seed=6, fill=1)
