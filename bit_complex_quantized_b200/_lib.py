@@ -510,6 +510,8 @@ class Kv4Cache:
         if records.dim() != 4 or records.shape[3] != 32 * dim + 256 or page_table.dim() != 2:
             raise ValueError(f"needs records [pages][kv_heads][page_tokens/16][{32 * dim + 256}] and page_table "
                              f"[B][table_cols], got {tuple(records.shape)} and {tuple(page_table.shape)}")
+        if not 1 <= n_new < 1 << 31:
+            _check(5)  # IFQ_ERR_BATCH
         pages, kv_heads, tiles = records.shape[:3]
         B = kv_lens.shape[0]
         self.dim, self.kv_heads, self.B, self.n_new = dim, kv_heads, B, n_new

@@ -345,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
       bool bad = false;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        bad |= !(fabsf(v[j]) <= 3.402823466e38f);
         v[j] *= p.scale2;
+        bad |= !(fabsf(v[j]) <= 3.402823466e38f);  // q or the scale
         mx = fmaxf(mx, fabsf(v[j]));
       }
 #pragma unroll

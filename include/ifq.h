@@ -547,11 +547,12 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *                    ldo apart.  score = scale Re(q^T conj(k)).  n_new <=
  *                    IFQ_KV4_MAX_NEW.  A row that sees no key is 0.  q enters as two fp16
  *                    terms (2^-22 of the row's largest entry), the weights times a value's scale as one
- *                    (2^-11 relative); sums and the softmax's maximum and sum are float32, and
- *                    stay finite for stored values up to 2^100; partial results are joined in a
- *                    fixed order (bit-reproducible).  A NaN or Inf in q,
- *                    or an entry with |scale q| above 2^99, sets IFQ_DEV_NONFINITE and makes
- *                    that row NaN.
+ *                    (2^-11 relative, or 2^-32 of the largest scale among the keys so far where
+ *                    that is more); sums and the softmax's maximum and sum are float32, and
+ *                    stay finite for stored values up to 2^100 and scores up to 2^126; partial
+ *                    results are joined in a fixed order (bit-reproducible).  A NaN or Inf in q
+ *                    or scale, or an entry with |scale q| above 2^99, sets IFQ_DEV_NONFINITE
+ *                    and makes that row NaN.
  *   workspace        device scratch of ifq_kv4_attention_workspace_bytes() bytes,
  *                    16-byte aligned, no initial contents needed; calls that share it
  *                    must not overlap on the GPU.  May be NULL when that is 0.

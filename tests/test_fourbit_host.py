@@ -137,6 +137,10 @@ def test_python_refuses_wrong_tensors():
     with pytest.raises(ValueError):
         Q.Kv4Cache(torch.zeros(2, 1, 1, 100, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.int32),
                    torch.zeros(1, dtype=torch.int32), 64)
+    for n_new in (0, -1, 1 << 32 | 1):
+        with pytest.raises(Q.IfqError):
+            Q.Kv4Cache(torch.zeros(2, 1, 1, 32 * 64 + 256, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.int32),
+                       torch.zeros(1, dtype=torch.int32), 64, n_new=n_new)
 
 
 # ------------------------------------------------------------------ the oracle against the definitions

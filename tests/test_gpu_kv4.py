@@ -332,6 +332,34 @@ def test_attention_huge_query_counts_as_not_finite():
     c.check(1, skip=(0,))
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_attention_scale_not_finite(scale):
+    c = Case([100], [2], 1, 64, 16, seed=25)
+    c.fill_random()
+    st = status_word()
+    c.attention(1, scale=scale, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.IFQ_DEV_NONFINITE
+    for x in c.o:
+        assert torch.isnan(x[:2]).all() and (x[2:] == 77.0).all()
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 24])
+def test_attention_value_outlier(ratio):
+    """A key with values `ratio` times larger than all others and a weight of almost nothing."""
+    c = Case([70], [1], 1, 64, 16, seed=26)
+    c.fill_random()
+    at = c.table[0, 1], 0, 0                     # token 16
+    par = c.records[at][32 * 64:].view(np.uint16).reshape(2, 16, 4)
+    par[1, 0] = F.bf16_bits(F.bf16_value(par[1, 0]) * np.float32(ratio))
+    par[0, 0, 1::2] = F.bf16_bits(np.full(2, -1e4, np.float32))     # its key: far below the others
+    c.d_records.copy_(to_dev(c.records))
+    q = [np.abs(c.rng.standard_normal((c.rows, 64))).astype(np.float32) for _ in range(2)]
+    c.attention(1, q=q)
+    torch.cuda.synchronize()
+    c.check(1)
+
+
 def test_attention_ignores_what_lies_behind():
     """NaN parameters and codes behind the last token, in its own record and in others, never reach an output."""
     c = Case([33, 7], [1, 2], 2, 64, 32, seed=4, fill=0xFF)
