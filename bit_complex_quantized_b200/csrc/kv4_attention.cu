@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
   const Kv4Arg& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = (int)blockIdx.x % p.cluster;
+  follow();
 
   // The runs.  Thread i counts the sequences i per_thread .. + per_thread - 1.
   __shared__ unsigned long long warp_sums[kWarps];
@@ -215,8 +216,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
       p.ws_cut[blockIdx.x].pair = -1;
     }
     __syncthreads();
-    // the joining kernel may take its place as this one's CTAs leave; it waits for their results
-    asm volatile("griddepcontrol.launch_dependents;");
   }
 
   for (;;) {
@@ -676,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constan
   __shared__ float os[kWarps][D];
   __shared__ float ls[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y, qr = gridDim.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the main kernel runs
+  follow();  // the main kernel's results
   const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.ws_cut + blockIdx.x));  // pair, first, last, n_new
   const longlong2 cut2 = __ldcg(reinterpret_cast<const longlong2*>(p.ws_cut + blockIdx.x) + 1);
   if (cut.x < 0) return;
@@ -763,35 +762,16 @@ cudaError_t launch_nt(const AttnParams& p, cudaStream_t s) {
   constexpr int bytes = Layout<DIM, NT>::kBytes;
   cudaError_t e = allow_smem(kernel, bytes, &done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = p.counted ? dim3((unsigned)p.counted)
-                          : dim3((unsigned)p.cluster, (unsigned)(p.c.kv_heads * p.qtiles), (unsigned)p.c.B);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)p.cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  const dim3 grid = p.counted ? dim3((unsigned)p.counted)
+                              : dim3((unsigned)p.cluster, (unsigned)(p.c.kv_heads * p.qtiles), (unsigned)p.c.B);
+  return launch_following<AttnParams>(kernel, grid, kThreads, bytes, p.cluster, p, s);
 }
 
 template <int DIM>
 cudaError_t launch(const AttnParams& p, const Plan& r, cudaStream_t s) {
   cudaError_t e = r.nt == 1 ? launch_nt<DIM, 1>(p, s) : launch_nt<DIM, 2>(p, s);
   if (e != cudaSuccess || !r.ctas) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)r.ctas, 4u * r.nt);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<DIM>, p);
+  return launch_following<AttnParams>(kv4_join_kernel<DIM>, dim3((unsigned)r.ctas, 4u * r.nt), kThreads, 0, 1, p, s);
 }
 
 }  // namespace

@@ -75,7 +75,7 @@ IFQ_DEVINL Group group_of(float lo, float hi) {
   Group r;
   r.s = __bfloat162float(sb);
   r.m = __bfloat162float(mb);
-  r.factor = code_factor(r.s, 1.0f / 15.0f, &r.fast);
+  r.factor = code_factor<true>(r.s, 1.0f / 15.0f, &r.fast);
   r.bits = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
   return r;
 }
@@ -84,7 +84,7 @@ IFQ_DEVINL uint32_t codes_of(const float4& x, const Group& q) {
   bool near = !q.fast;
   const float4 d = make_float4(x.x - q.m, x.y - q.m, x.z - q.m, x.w - q.m);
   const uint32_t w = fast_codes4<15>(d, q.factor, 0.0f, 0.0f, &near);
-  return near ? exact_codes4(x, q.s, q.m, 0.0f, 15.0f, 0.0f) : w;
+  return near ? exact_codes4<true>(x, q.s, q.m, 0.0f, 15.0f, 0.0f) : w;
 }
 // The word of eight entries of a key: entries 0, 2, 4, 6 in the low half, 1, 3, 5, 7 in the high half.
 IFQ_DEVINL uint32_t key_word(const float4& a, const float4& b, const Group& q) {
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_tokens_kernel(const __gri
   constexpr int LP = DIM / 8, D = 2 * DIM;
   const Kv4Arg& c = p.c;
   const int b = blockIdx.y;
+  follow();
   const Kv4Seq q = kv4_seq(c, b);
   if (!q.ok) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
@@ -178,6 +179,7 @@ template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __grid_constant__ AppendParams p) {
   constexpr int D = 2 * DIM, CP = DIM / 32;
   static_assert(kWarps == 4, "a warp per plane");
+  follow();
   const Kv4Seq seq = kv4_seq(p.c, blockIdx.z);
   if (!seq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   Item it;
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __gr
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) kv4_read_records_kernel(const __grid_constant__ AppendParams p) {
   constexpr int D = 2 * DIM, CH = D / 32, CP = DIM / 32;
+  follow();
   const Kv4Seq seq = kv4_seq(p.c, blockIdx.z);
   if (!seq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   const int head = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -353,6 +356,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_tokens_kernel(const __grid_
   constexpr int LP = DIM / 8, D = 2 * DIM;
   const Kv4Arg& c = p.c;
   const int b = blockIdx.y;
+  follow();
   const Kv4Seq q = kv4_seq(c, b);
   if (!q.ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   const int idx = blockIdx.x * kThreads + threadIdx.x;
@@ -398,16 +402,16 @@ cudaError_t launch(const AppendParams& p, bool read, cudaStream_t s) {
   if (tokens) {  // threads of 8 entries
     const int64_t blocks = ((int64_t)p.c.n_new * p.c.kv_heads * (DIM / 2) + kThreads - 1) / kThreads;
     const dim3 grid((unsigned)blocks, (unsigned)p.c.B);
-    if (read) kv4_read_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
-    else kv4_append_tokens_kernel<DIM><<<grid, kThreads, 0, s>>>(p);
+    auto kernel = read ? kv4_read_tokens_kernel<DIM> : kv4_append_tokens_kernel<DIM>;
+    return launch_following<AppendParams>(kernel, grid, kThreads, 0, 1, p, s);
   } else {       // the records that n_new tokens can touch, a CTA (appending) or a warp each; heads fastest, so that
                  // CTAs that run together read neighbouring columns
     const unsigned tiles = (unsigned)(((int64_t)p.c.n_new + 14) / 16 + 1);
     const unsigned heads = (unsigned)p.c.kv_heads;
-    if (read) kv4_read_records_kernel<DIM><<<dim3((heads + kWarps - 1) / kWarps, tiles, p.c.B), kThreads, 0, s>>>(p);
-    else kv4_append_records_kernel<DIM><<<dim3(heads, tiles, p.c.B), kThreads, 0, s>>>(p);
+    auto kernel = read ? kv4_read_records_kernel<DIM> : kv4_append_records_kernel<DIM>;
+    const dim3 grid(read ? (heads + kWarps - 1) / kWarps : heads, tiles, (unsigned)p.c.B);
+    return launch_following<AppendParams>(kernel, grid, kThreads, 0, 1, p, s);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t dispatch(const ifq_kv4_cache& c, const AppendParams& p, bool read, cudaStream_t s) {

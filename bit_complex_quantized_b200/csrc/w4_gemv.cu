@@ -14,9 +14,9 @@
 // no workspace, a fixed order of sums.
 //
 // Bound: a word takes 5 integer, 4 bf16 and 1 (2 above 8 tokens) matrix instructions and with loads, scales and
-// copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 21.3 us,
-// 76 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
-// groups of 32, 5 tokens: 26 us, 69 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
+// copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 20.9 us,
+// 78 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
+// groups of 32, 5 tokens: 25.4 us, 71 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
 // the layer set 117 us, 59 %: issue at 12 to 16 warps an SM (the accumulators and operands of 16 tokens fill the
 // registers).
 #include "ifq_internal.h"
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas))
   const uint16_t* x_src = second ? L.x[1] + xt * (L.cols - L.x_split) + (xk - L.x_split) : L.x[0] + xt * L.x_split + xk;
   int64_t x_step = kXTokens * (second ? L.cols - L.x_split : L.x_split);
   const uint32_t ring = smem_u32(smem) + warp * R::kStages * R::kStage;
+  follow();
   const uint32_t code_dst = ring + lane * 16, scale_dst = ring + R::kCodes + lane * 16;
   const uint32_t x_dst = smem_u32(smem) + R::kXRing + col_warp * R::kStages * R::kX +
                          ((xv >> 2) * XB * 4 + (xv & 3)) * 16 + xt * 64;
@@ -421,18 +422,7 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
     const int64_t each = cluster / l.split;  // row tiles of a cluster
     clusters += (l.tiles + each - 1) / each;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = R::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return launch_following<LParams<kCap>>(kernel, dim3((unsigned)(clusters * cluster)), kThreads, R::kBytes, cluster, p, s);
 }
 
 template <int G, int kCap>

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
       sbits[h] = __bfloat16_as_ushort(sb);
       const float s = __bfloat162float(sb);
       bool fast;
-      const float factor = code_factor(s, 1.0f / 14.0f, &fast);
+      const float factor = code_factor<false>(s, 1.0f / 14.0f, &fast);
       constexpr float kOnes = 1 + 16 + 256 + 4096;  // codes are stored plus 8; q + 7 = 14 (w / (14 s) + 1/2)
 #pragma unroll
       for (int c = c0g; c < c0g + kPer; ++c) {
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
           const float4 x = i == 0 ? make_float4(a.x, a.z, b.x, b.z) : make_float4(a.y, a.w, b.y, b.w);
           bool near = !fast;
           half[i] = fast_codes4<14>(x, factor, 0.5f, kOnes, &near);
-          if (near) half[i] = exact_codes4(x, s, 0.0f, -7.0f, 7.0f, 8.0f * kOnes);
+          if (near) half[i] = exact_codes4<false>(x, s, 0.0f, -7.0f, 7.0f, 8.0f * kOnes);
         }
         words[h][c] = half[0] | (half[1] << 16);
       }
