@@ -10,15 +10,17 @@
 //           words and half words alone: as many threads as there are entries, the shortest chain.  16 sequences of
 //           8 heads, appending and reading back: 5.5 us, against 26.6 us by records (a warp then has one live
 //           token of 16 in a chain 16 times as long).
-//   16 and more (prompts)   a warp takes one plane of one record (16 tokens of a head): keys as lane (g, t) holds them
+//   16 and more (prompts)   a warp takes one plane of a record (16 tokens of a head) and then the next heads' (up to 8,
+//           so that lengths, pages and places are found once): keys as lane (g, t) holds them
 //           in the record (8 entries of the tokens g and g + 8 per 32 columns), values likewise (4 entries of
-//           four tokens), so that loads are 128-byte runs, a plane's minimum and maximum take two or three
-//           shuffles, and a record that is all new leaves as 512-byte stores.  A record that holds older tokens
+//           four tokens), so that loads are 128-byte runs, and a record that is all new leaves as 512-byte stores.
+//           The lanes of a plane share out its minima and maxima as they join them, so each makes one group's
+//           parameters.  A record that holds older tokens
 //           too is written token by token: a token's keys are whole words and its values whole half words, so
-//           nothing is read back.  93 thousand tokens x heads of dim 64, appending and reading back: 49 us (203 MB,
-//           4.1 TB/s), against 149 us by tokens (scattered 2 and 4 byte stores).
-// HBM-bound in bytes (16 dim read and 2 dim + 16 written per token and head); appending issues about 27
-// instructions per entry, which with the latency of short CTAs keeps it at two thirds of the copy rate.
+//           nothing is read back.  93 thousand tokens x heads of dim 64, appending and reading back: 44 us (203 MB,
+//           4.6 TB/s), against 149 us by tokens (scattered 2 and 4 byte stores).
+// HBM-bound in bytes (16 dim read and 2 dim + 16 written per token and head): 20000 tokens of 32 heads are appended in
+// 122 us, 95 % of the copy rate (131 us without the prefetch of the next head).  Appending issues 15 instructions per entry.
 #include "ifq_internal.h"
 #include "kv4_common.cuh"
 
@@ -33,6 +35,7 @@ struct AppendParams {
   const float* src[4];  // k_re, k_im, v_re, v_im
   float* dst[4];        // the same, for reading back
   int64_t ld;
+  int32_t heads_each;   // heads that a CTA appends one after the other
   uint32_t* status;
 };
 
@@ -79,10 +82,32 @@ IFQ_DEVINL Group group_of(float lo, float hi) {
   r.bits = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
   return r;
 }
+// The group that lane `from` of the warp holds.
+IFQ_DEVINL Group group_from(const Group& own, int from) {
+  Group r;
+  r.bits = __shfl_sync(0xffffffffu, own.bits, from);
+  r.factor = __shfl_sync(0xffffffffu, own.factor, from);
+  r.s = bf16_lo(r.bits);
+  r.m = bf16_hi(r.bits);
+  r.fast = code_factor_usable<true>(r.s);
+  return r;
+}
+// Minima and maxima of two groups, over lanes that differ in bit `mask`: the lane whose bit is set goes on with the
+// second group, the other with the first.
+IFQ_DEVINL void halve(float lo0, float lo1, float hi0, float hi1, int mask, bool second, float* lo, float* hi) {
+  *lo = fminf(second ? lo1 : lo0, __shfl_xor_sync(0xffffffffu, second ? lo0 : lo1, mask));
+  *hi = fmaxf(second ? hi1 : hi0, __shfl_xor_sync(0xffffffffu, second ? hi0 : hi1, mask));
+}
+IFQ_DEVINL void both(float* lo, float* hi, int mask) {
+  *lo = fminf(*lo, __shfl_xor_sync(0xffffffffu, *lo, mask));
+  *hi = fmaxf(*hi, __shfl_xor_sync(0xffffffffu, *hi, mask));
+}
 // Entry j of four in bits 4 j.
 IFQ_DEVINL uint32_t codes_of(const float4& x, const Group& q) {
   bool near = !q.fast;
-  const float4 d = make_float4(x.x - q.m, x.y - q.m, x.z - q.m, x.w - q.m);
+  const uint64_t minus_m = pair(-q.m);
+  const float2 d0 = halves(add2(pair(x.x, x.y), minus_m)), d1 = halves(add2(pair(x.z, x.w), minus_m));
+  const float4 d = make_float4(d0.x, d0.y, d1.x, d1.y);
   const uint32_t w = fast_codes4<15>(d, q.factor, 0.0f, 0.0f, &near);
   return near ? exact_codes4<true>(x, q.s, q.m, 0.0f, 15.0f, 0.0f) : w;
 }
@@ -94,11 +119,10 @@ IFQ_DEVINL uint32_t key_word(const float4& a, const float4& b, const Group& q) {
 IFQ_DEVINL float4 take(const float* src, bool in) {
   return in ? __ldcs(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
-// Minimum and maximum so far; odd becomes NaN with a NaN or Inf entry.
-IFQ_DEVINL void widen(const float4& v, float* lo, float* hi, float* odd) {
-  *lo = fminf(*lo, fminf(fminf(v.x, v.y), fminf(v.z, v.w)));
-  *hi = fmaxf(*hi, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-  *odd = fmaf(v.x, 0.0f, fmaf(v.y, 0.0f, fmaf(v.z, 0.0f, fmaf(v.w, 0.0f, *odd))));
+// Minimum and maximum so far, NaN with a NaN entry.
+IFQ_DEVINL void widen(const float4& v, float* lo, float* hi) {
+  *lo = min3(min3(*lo, v.x, v.y), v.z, v.w);
+  *hi = max3(max3(*hi, v.x, v.y), v.z, v.w);
 }
 // NaN and Inf become 0 (*bad), larger magnitudes the largest bf16.
 IFQ_DEVINL void tame(float4& v, bool* bad) {
@@ -113,7 +137,7 @@ IFQ_DEVINL void tame(float4& v, bool* bad) {
   }
 }
 // Whether a lane's entries need tame().
-IFQ_DEVINL bool wild(float lo, float hi, float odd) { return !(odd == 0.0f) || lo < -kBf16Max || hi > kBf16Max; }
+IFQ_DEVINL bool wild(float lo, float hi) { return !(lo >= -kBf16Max && hi <= kBf16Max); }
 
 // One token's plane, 8 entries a thread.
 template <int DIM>
@@ -137,16 +161,16 @@ __global__ void __launch_bounds__(kThreads) kv4_append_tokens_kernel(const __gri
   const float* src = p.src[plane] + (q.row0 + tok) * p.ld + head * DIM + part * 8;
   x[0] = take(src, live);
   x[1] = take(src + 4, live);
-  float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
-  widen(x[0], &lo, &hi, &odd);
-  widen(x[1], &lo, &hi, &odd);
+  float lo = INFINITY, hi = -INFINITY;
+  widen(x[0], &lo, &hi);
+  widen(x[1], &lo, &hi);
   bool bad = false;
-  if (wild(lo, hi, odd)) {
+  if (wild(lo, hi)) {
     tame(x[0], &bad);
     tame(x[1], &bad);
     lo = INFINITY, hi = -INFINITY;
-    widen(x[0], &lo, &hi, &odd);
-    widen(x[1], &lo, &hi, &odd);
+    widen(x[0], &lo, &hi);
+    widen(x[1], &lo, &hi);
   }
 #pragma unroll
   for (int o = 1; o < LP; o *= 2) {
@@ -174,119 +198,146 @@ __global__ void __launch_bounds__(kThreads) kv4_append_tokens_kernel(const __gri
   if (part == 0) *reinterpret_cast<uint32_t*>(rec + 16 * D + (plane >> 1) * 128 + r * 8 + (plane & 1) * 4) = gq.bits;
 }
 
-// One plane of a record's keys (planes 0, 1) or values (2, 3): warp w of the CTA takes plane w.
+// One plane of the keys (planes 0, 1) or values (2, 3) of a record of p.heads_each heads: warp w of the CTA takes plane w.
+constexpr int records_ctas(int dim) { return dim == 128 ? 3 : 5; }  // that an SM holds
+
 template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv4_append_records_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, records_ctas(DIM))
+    kv4_append_records_kernel(const __grid_constant__ AppendParams p) {
   constexpr int D = 2 * DIM, CP = DIM / 32;
   static_assert(kWarps == 4, "a warp per plane");
   follow();
   const Kv4Seq seq = kv4_seq(p.c, blockIdx.z);
   if (!seq.ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(p.status, IFQ_DEV_RANGE);
   Item it;
-  if (!find_item(p, seq, blockIdx.y, blockIdx.x, &it) || !it.rec) return;
+  if (!find_item(p, seq, blockIdx.y, blockIdx.x * p.heads_each, &it) || !it.rec) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, plane = threadIdx.x >> 5, pl = plane & 1;
   const int32_t len = it.q.len;
   auto in = [&](int r) { return it.pos0 + r >= it.first && it.pos0 + r < len; };
   const float* src = p.src[plane] + (it.q.row0 + it.pos0 - it.first) * p.ld + it.head * DIM;
   const bool all = in(0) && in(15);
   bool bad = false;
-  uint32_t* par = reinterpret_cast<uint32_t*>(it.rec + 16 * D) + (plane >> 1) * 32 + pl;
-  uint32_t words[CP][2];  // {32-column chunk of the plane, h}
-  if (plane < 2) {        // keys: tokens g + 8 h, entries 8 t .. 8 t + 7 of a chunk
-    float4 v[2][CP][2];
+  const int heads = min(p.heads_each, p.c.kv_heads - it.head);
+#pragma unroll 1
+  for (int head = 0; head < heads; ++head, src += DIM, it.rec += p.c.page_tiles * p.c.record_bytes) {
+    if (head + 1 < heads) {  // the next head's lines on their way to L2
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int i = lane; i < DIM / 2; i += 32) {
+        const int r = i / CP;
+        if (in(r)) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + DIM + r * p.ld + i % CP * 32));
+      }
+    }
+    uint32_t* par = reinterpret_cast<uint32_t*>(it.rec + 16 * D) + (plane >> 1) * 32 + pl;
+    uint32_t words[CP][2];  // {32-column chunk of the plane, h}
+    // The lanes of a group halve the groups that they share at each step of its minimum and maximum, so that a lane ends
+    // with one group, makes its parameters and hands them back.
+    if (plane < 2) {        // keys: tokens g + 8 h, entries 8 t .. 8 t + 7 of a chunk
+      float4 v[2][CP][2];
 #pragma unroll
-      for (int c = 0; c < CP; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v[h][c][i] = take(src + (g + 8 * h) * p.ld + c * 32 + t * 8 + i * 4, in(g + 8 * h));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CP; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) widen(v[h][c][i], &lo, &hi, &odd);
-      if (wild(lo, hi, odd)) {
-        lo = INFINITY, hi = -INFINITY;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < CP; ++c)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            tame(v[h][c][i], &bad);
-            widen(v[h][c][i], &lo, &hi, &odd);
-          }
+          for (int i = 0; i < 2; ++i)
+            v[h][c][i] = take(src + (g + 8 * h) * p.ld + c * 32 + t * 8 + i * 4, in(g + 8 * h));
+      float lo[2], hi[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lo[h] = INFINITY, hi[h] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) widen(v[h][c][i], &lo[h], &hi[h]);
+        if (wild(lo[h], hi[h])) {
+          lo[h] = INFINITY, hi[h] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < CP; ++c)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              tame(v[h][c][i], &bad);
+              widen(v[h][c][i], &lo[h], &hi[h]);
+            }
+        }
       }
+      float l, u;
+      halve(lo[0], lo[1], hi[0], hi[1], 1, t & 1, &l, &u);
+      both(&l, &u, 2);
+      const Group own = group_of(l, u);  // of token g + 8 (t % 2)
+      if (t < 2 && in(g + 8 * t)) par[(g + 8 * t) * 2] = own.bits;
 #pragma unroll
-      for (int o = 1; o < 4; o *= 2) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      for (int h = 0; h < 2; ++h) {
+        const Group q = group_from(own, (lane & ~3) + h);
+#pragma unroll
+        for (int c = 0; c < CP; ++c) words[c][h] = key_word(v[h][c][0], v[h][c][1], q);
       }
-      const Group q = group_of(lo, hi);
-#pragma unroll
-      for (int c = 0; c < CP; ++c) words[c][h] = key_word(v[h][c][0], v[h][c][1], q);
-      if (t == 0 && in(g + 8 * h)) par[(g + 8 * h) * 2] = q.bits;
-    }
-  } else {                // values: tokens 2 t + 8 h + e, entries 4 g .. 4 g + 3 of a chunk
-    float4 v[2][2][CP];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int c = 0; c < CP; ++c) {
-          const int r = 2 * t + 8 * h + e;
-          v[h][e][c] = take(src + r * p.ld + c * 32 + g * 4, in(r));
-        }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 2 * t + 8 * h + e;
-        float lo = INFINITY, hi = -INFINITY, odd = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CP; ++c) widen(v[h][e][c], &lo, &hi, &odd);
-        if (wild(lo, hi, odd)) {
-          lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < CP; ++c) {
-            tame(v[h][e][c], &bad);
-            widen(v[h][e][c], &lo, &hi, &odd);
-          }
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        const Group q = group_of(lo, hi);
-#pragma unroll
-        for (int c = 0; c < CP; ++c) {
-          const uint32_t w = codes_of(v[h][e][c], q) << (16 * e);
-          words[c][h] = e == 0 ? w : words[c][h] | w;
-        }
-        if (g == 0 && in(r)) par[r * 2] = q.bits;
-      }
-  }
-#pragma unroll
-  for (int c = 0; c < CP; ++c) {  // chunk ch is the words 2 (ch % 2) + h of the 16 bytes of its pair of chunks
-    const int ch = pl * CP + c;
-    uint8_t* dst = it.rec + (plane >> 1) * 8 * D + (ch >> 1) * 512 + lane * 16 + (ch & 1) * 8;
-    if (all && CP > 1) {
-      const int even = c - (CP > 1);
-      if (c & 1)
-        *reinterpret_cast<uint4*>(dst - 8) = make_uint4(words[even][0], words[even][1], words[c][0], words[c][1]);
-    } else if (all) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(words[c][0], words[c][1]);
-    } else if (plane < 2) {
+    } else {                // values: tokens 2 t + 8 h + e, entries 4 g .. 4 g + 3 of a chunk
+      float4 v[2][2][CP];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (in(g + 8 * h)) reinterpret_cast<uint32_t*>(dst)[h] = words[c][h];
-    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)  // half words: token 2 t + 8 h + (e & 1)
-        if (in(2 * t + 8 * (e >> 1) + (e & 1)))
-          reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(words[c][e >> 1] >> (16 * (e & 1)));
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int c = 0; c < CP; ++c) {
+            const int r = 2 * t + 8 * h + e;
+            v[h][e][c] = take(src + r * p.ld + c * 32 + g * 4, in(r));
+          }
+      float lo[2][2], hi[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          lo[h][e] = INFINITY, hi[h][e] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < CP; ++c) widen(v[h][e][c], &lo[h][e], &hi[h][e]);
+          if (wild(lo[h][e], hi[h][e])) {
+            lo[h][e] = INFINITY, hi[h][e] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < CP; ++c) {
+              tame(v[h][e][c], &bad);
+              widen(v[h][e][c], &lo[h][e], &hi[h][e]);
+            }
+          }
+        }
+      const int h_own = g >> 2, e_own = (g >> 1) & 1, r_own = 2 * t + 8 * h_own + e_own;
+      float l2[2], u2[2], l, u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) halve(lo[0][e], lo[1][e], hi[0][e], hi[1][e], 16, h_own, &l2[e], &u2[e]);
+      halve(l2[0], l2[1], u2[0], u2[1], 8, e_own, &l, &u);
+      both(&l, &u, 4);
+      const Group own = group_of(l, u);  // of token r_own
+      if (!(g & 1) && in(r_own)) par[r_own * 2] = own.bits;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Group q = group_from(own, 16 * h + 8 * e + t);
+#pragma unroll
+          for (int c = 0; c < CP; ++c) {
+            const uint32_t w = codes_of(v[h][e][c], q) << (16 * e);
+            words[c][h] = e == 0 ? w : words[c][h] | w;
+          }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {  // chunk ch is the words 2 (ch % 2) + h of the 16 bytes of its pair of chunks
+      const int ch = pl * CP + c;
+      uint8_t* dst = it.rec + (plane >> 1) * 8 * D + (ch >> 1) * 512 + lane * 16 + (ch & 1) * 8;
+      if (all && CP > 1) {
+        const int even = c - (CP > 1);
+        if (c & 1)
+          *reinterpret_cast<uint4*>(dst - 8) = make_uint4(words[even][0], words[even][1], words[c][0], words[c][1]);
+      } else if (all) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(words[c][0], words[c][1]);
+      } else if (plane < 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (in(g + 8 * h)) reinterpret_cast<uint32_t*>(dst)[h] = words[c][h];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // half words: token 2 t + 8 h + (e & 1)
+          if (in(2 * t + 8 * (e >> 1) + (e & 1)))
+            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(words[c][e >> 1] >> (16 * (e & 1)));
+      }
     }
   }
   if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
@@ -409,8 +460,16 @@ cudaError_t launch(const AppendParams& p, bool read, cudaStream_t s) {
     const unsigned tiles = (unsigned)(((int64_t)p.c.n_new + 14) / 16 + 1);
     const unsigned heads = (unsigned)p.c.kv_heads;
     auto kernel = read ? kv4_read_records_kernel<DIM> : kv4_append_records_kernel<DIM>;
-    const dim3 grid(read ? (heads + kWarps - 1) / kWarps : heads, tiles, (unsigned)p.c.B);
-    return launch_following<AppendParams>(kernel, grid, kThreads, 0, 1, p, s);
+    AppendParams pp = p;
+    // up to 8 heads, as long as the GPU's places are taken twice (2900 tokens of 32 heads 22.2 us, with 1 head 27.3;
+    // with 16, which take them once, 34)
+    pp.heads_each = 8;
+    while (pp.heads_each > 1 && (int64_t)p.c.B * tiles * ((heads + pp.heads_each - 1) / pp.heads_each) <
+                                    2 * 148 * records_ctas(DIM))
+      pp.heads_each /= 2;
+    const unsigned each = read ? kWarps : (unsigned)pp.heads_each;
+    return launch_following<AppendParams>(kernel, dim3((heads + each - 1) / each, tiles, (unsigned)p.c.B), kThreads, 0,
+                                          1, pp, s);
   }
 }
 
@@ -424,13 +483,13 @@ cudaError_t dispatch(const ifq_kv4_cache& c, const AppendParams& p, bool read, c
 
 cudaError_t launch_kv4_append(const ifq_kv4_cache& c, const float* k_re, const float* k_im, const float* v_re,
                               const float* v_im, int64_t ld, uint32_t* dev_status, cudaStream_t s) {
-  AppendParams p = {kv4_arg(c), {k_re, k_im, v_re, v_im}, {}, ld, dev_status};
+  AppendParams p = {kv4_arg(c), {k_re, k_im, v_re, v_im}, {}, ld, 1, dev_status};
   return dispatch(c, p, false, s);
 }
 
 cudaError_t launch_kv4_read(const ifq_kv4_cache& c, float* k_re, float* k_im, float* v_re, float* v_im, int64_t ld,
                             uint32_t* dev_status, cudaStream_t s) {
-  AppendParams p = {kv4_arg(c), {}, {k_re, k_im, v_re, v_im}, ld, dev_status};
+  AppendParams p = {kv4_arg(c), {}, {k_re, k_im, v_re, v_im}, ld, 1, dev_status};
   return dispatch(c, p, true, s);
 }
 

@@ -78,22 +78,55 @@ IFQ_DEVINL float exact_code(float x, float s, float m, float lo, float hi) {
   return fminf(fmaxf(n, lo), hi);
 }
 
+// Two floats in a register pair, and arithmetic on both at once.
+IFQ_DEVINL uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+IFQ_DEVINL uint64_t pair(float both) { return pair(both, both); }
+IFQ_DEVINL float2 halves(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+IFQ_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+IFQ_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// Largest and smallest of three; NaN where one is NaN.
+IFQ_DEVINL float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+IFQ_DEVINL float min3(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Four codes n_j = rint(kSpan r_j), r = a d + bias saturated to [0, 1], as the number n0 + 16 n1 + 256 n2 + 4096 n3 +
-// base in bits 0-15 of the result.  kSpan r is within 2^-18 of the quotient that it stands for, so *near is set
+// base in bits 0-15 of the result.  kSpan r is within 2^-17 of the quotient that it stands for, so *near is set
 // where that could decide the rounding (then exact_codes4 gives the answer).
 template <int kSpan>
 IFQ_DEVINL uint32_t fast_codes4(const float4& d, float a, float bias, float base, bool* near) {
   constexpr float kMagic = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer
-  float sum = base;
-  const float* f = &d.x;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float r = __saturatef(fmaf(f[j], a, bias));
-    const float n = fmaf(r, (float)kSpan, kMagic) - kMagic;
-    *near |= fabsf(fmaf(r, (float)kSpan, -n)) > 0.49999f;
-    sum = fmaf(n, (float)(1 << (4 * j)), sum);
-  }
-  return __float_as_uint(sum + 8388608.0f) & 0xFFFFu;
+  const uint64_t span = pair((float)kSpan), magic = pair(kMagic), minus = pair(-1.0f);
+  const uint64_t r0 = pair(__saturatef(fmaf(d.x, a, bias)), __saturatef(fmaf(d.y, a, bias)));
+  const uint64_t r1 = pair(__saturatef(fmaf(d.z, a, bias)), __saturatef(fmaf(d.w, a, bias)));
+  const uint64_t n0 = fma2(fma2(r0, span, magic), minus, magic);  // -n
+  const uint64_t n1 = fma2(fma2(r1, span, magic), minus, magic);
+  const float2 e0 = halves(fma2(r0, span, n0)), e1 = halves(fma2(r1, span, n1));
+  *near |= fmaxf(max3(fabsf(e0.x), fabsf(e0.y), fabsf(e1.x)), fabsf(e1.y)) > 0.49999f;
+  const float2 u = halves(fma2(n1, pair(256.0f), n0));
+  return __float_as_uint(fmaf(u.y, -16.0f, base + 8388608.0f) - u.x) & 0xFFFFu;
 }
 // v 2^-8, which keeps the sign of the smallest numbers: of those only the side of a half that they are on matters.
 IFQ_DEVINL float shrink(float v) {
@@ -116,9 +149,15 @@ static __device__ __noinline__ uint32_t exact_codes4(float4 x, float s, float m,
 // A group's factor 1 / (span s) for fast_codes4 (0 where s = 0), and whether it is usable (not for scales so
 // small that it overflows, or so large that x - m may).
 template <bool kMin>
+IFQ_DEVINL bool code_factor_usable(float s) {
+  return s == 0.0f || (s >= 1e-30f && (!kMin || s <= kWideScale));
+}
+template <bool kMin>
 IFQ_DEVINL float code_factor(float s, float inv_span, bool* usable) {
-  *usable = s == 0.0f || (s >= 1e-30f && (!kMin || s <= kWideScale));
-  return s >= 1e-30f ? __frcp_rn(s) * inv_span : 0.0f;
+  *usable = code_factor_usable<kMin>(s);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // within 2^-23
+  return s >= 1e-30f ? r * inv_span : 0.0f;
 }
 
 IFQ_DEVINL float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

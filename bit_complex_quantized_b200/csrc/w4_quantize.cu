@@ -7,7 +7,8 @@
 // was rounded down (at most s 7 2^-9 more).
 //
 // HBM-bound: 4 bytes read and 0.5 + 2 / G written per weight.  Quantizing and dequantizing 10007 x 11008 in
-// groups of 32 (723 MB) takes 129 us, 87 % of the copy rate; 4096 x 4096 (109 MB, two launches) 24 us, 71 %.
+// groups of 32 (723 MB) takes 120 us, 93 % of the copy rate; 4096 x 4096 (109 MB, two launches) 21.5 us, 79 %.  CTAs of 128 threads: of 256,
+// two fit on an SM in groups of 128 (95 registers), 23.0 us.
 // A warp takes 16 rows x max(64, G) columns, so that every group's maximum stays inside four lanes, loads are
 // 32-byte runs per lane that fill whole 128-byte lines across a quad of lanes, and the codes leave as one
 // 512-byte store per tile.
@@ -17,7 +18,7 @@
 namespace ifq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 struct QArg {
@@ -75,21 +76,19 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
     uint32_t sbits[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // odd becomes NaN with a NaN or Inf weight, which the maximum alone would not show
-      auto largest = [&](float* odd) {
+      auto largest = [&] {  // NaN or Inf with such a weight
         float m = 0.0f;
 #pragma unroll
         for (int c = c0g; c < c0g + kPer; ++c)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float4& x = v[h][c][i];
-            m = fmaxf(m, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-            *odd = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, fmaf(x.w, 0.0f, *odd))));
+            m = max3(max3(m, fabsf(x.x), fabsf(x.y)), fabsf(x.z), fabsf(x.w));
           }
         return m;
       };
-      float odd = 0.0f, m = largest(&odd);
-      if (!(odd == 0.0f)) {
+      float m = largest();
+      if (!(m <= 3.402823466e38f)) {
         bad = true;
 #pragma unroll
         for (int c = c0g; c < c0g + kPer; ++c)
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) w4_quant_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = fabsf(f[j]) <= 3.402823466e38f ? f[j] : 0.0f;
           }
-        m = largest(&odd);
+        m = largest();
       }
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));

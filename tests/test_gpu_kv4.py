@@ -193,6 +193,34 @@ def test_append_widest_groups(new):
     np.testing.assert_array_equal(c.d_records.cpu().numpy(), c.records)
 
 
+@pytest.mark.parametrize("B,heads,dim,page", [(64, 9, 32, 48), (90, 5, 64, 16), (128, 3, 32, 64), (50, 16, 128, 32)])
+def test_append_many_heads_at_once(B, heads, dim, page):
+    """Prompts large enough for several heads a block leave the records that appending 15 tokens at a time leaves."""
+    rng = np.random.default_rng(B)
+    news = [int(rng.integers(0, 200)) for _ in range(B - 1)] + [200]
+    lens = [n + int(rng.integers(0, 40)) for n in news]
+    c = Case(lens, news, heads, dim, page, seed=B, fill=0x5A)
+    x = [torch.randn(c.rows, heads * dim, device=DEV) for _ in range(4)]
+    x[0][3, 5], x[2][7, 1] = float("nan"), float("inf")
+    st = status_word()
+    Q.ifq_kv4_append(c.cache, *x, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.IFQ_DEV_NONFINITE
+    have = c.d_records.clone()
+    c.d_records.copy_(to_dev(c.records))
+    for done in range(0, 200, 15):
+        part = [min(15, max(0, n - done)) for n in news]
+        rows = torch.cat([torch.arange(c.offs[b] + done, c.offs[b] + done + n) for b, n in enumerate(part)]).to(DEV)
+        if len(rows) == 0:
+            break
+        upto = np.array([length - new + min(new, done + 15) for length, new in zip(lens, news)], np.int32)
+        offs = np.concatenate([[0], np.cumsum(part)]).astype(np.int32)
+        cache = Q.Kv4Cache(c.d_records, c.d_table, to_dev(upto), dim, n_new=15, rows=len(rows), new_offsets=to_dev(offs))
+        Q.ifq_kv4_append(cache, *[p[rows].contiguous() for p in x])
+    torch.cuda.synchronize()
+    assert torch.equal(have, c.d_records)
+
+
 def test_append_takes_column_slices():
     """k and v as column slices of one wide output (a fused q, k, v product)."""
     c = Case([5, 9], [2, 1], 2, 64, 16, seed=6, fill=1)
