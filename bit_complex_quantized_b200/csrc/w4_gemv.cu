@@ -17,8 +17,9 @@
 // copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 20.9 us,
 // 78 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
 // groups of 32, 5 tokens: 25.4 us, 71 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
-// the layer set 117 us, 59 %: issue at 12 to 16 warps an SM (the accumulators and operands of 16 tokens fill the
-// registers).
+// the layer set 117 us, 59 %: a matrix instruction takes 8 cycles of a quarter SM and does not run beside the FMA pipe
+// (both measured), so a word's 2 products, 4 conversions and 2 scalings fill the 22 cycles in which HBM delivers it, and
+// the 12 to 16 warps an SM whose registers 16 tokens leave room for keep them at 55 to 60 %.
 #include "ifq_internal.h"
 #include "q4_common.cuh"
 
