@@ -372,6 +372,20 @@ def test_attention_scale_not_finite(scale):
         assert torch.isnan(x[:2]).all() and (x[2:] == 77.0).all()
 
 
+@pytest.mark.parametrize("B", [1024, 1025])
+def test_attention_more_sequences_than_are_counted(B):
+    """The most sequences whose runs are counted, and one more: a block per pair whatever the lengths."""
+    lens, news = [1 + b % 4 for b in range(B)], [1] * B
+    lens[B - 1], lens[100], lens[1], news[1] = 3001, 999, 0, 0
+    c = Case(lens, news, 2, 32, 16, seed=B)
+    c.fill_random()
+    st = status_word()
+    c.attention(2, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    c.check(2)
+
+
 @pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 24])
 def test_attention_value_outlier(ratio):
     """A key with values `ratio` times larger than all others and a weight of almost nothing."""
