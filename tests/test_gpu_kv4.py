@@ -373,7 +373,7 @@ def test_attention_scale_not_finite(scale):
 
 
 @pytest.mark.parametrize("B", [1024, 1025])
-def test_attention_more_sequences_than_are_counted(B):
+def test_attention_most_sequences_that_are_counted(B):
     """The most sequences whose runs are counted, and one more: a block per pair whatever the lengths."""
     lens, news = [1 + b % 4 for b in range(B)], [1] * B
     lens[B - 1], lens[100], lens[1], news[1] = 3001, 999, 0, 0
