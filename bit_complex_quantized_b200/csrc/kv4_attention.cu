@@ -31,10 +31,10 @@
 //               parts each 79 us).
 // All joins add in a fixed order.
 //
-// Bound: 131072 tokens of 8 heads (64 query heads, 151 MB) take 45 us, 3.3 TB/s.  Of that about 8 us are the
-// launches, the first copies and the joins.  The loop issues 280 warp instructions per record and pair of 8 rows (80 to
-// unmask codes, 32 matrix instructions, 60 for scores and weights) at half the issue rate, 12 warps an SM: the copies
-// alone would take 33 us, the arithmetic alone 33 us, each with the fixed part.
+// Bound: 131072 tokens of 8 heads (64 query heads, 151 MB) take 41 us.  About 15 us of that do not grow with the length:
+// two launches, counting, a pair's q and first copies, the joins.  Each further 131072 tokens take 26 us (89 % of the
+// copy rate); the loop's arithmetic alone takes as long: 280 warp instructions per record and pair of 8 rows (80 to unmask
+// codes, 24 matrix instructions, 60 for scores and weights) at half the issue rate.
 #include "ifq_internal.h"
 #include "kv4_common.cuh"
 
@@ -63,13 +63,15 @@ struct AttnParams {
   int32_t shared;    // query heads of a key/value head
   int32_t cluster, qtiles;
   int32_t counted;   // equal runs of the units of all pairs (else a cluster per pair)
+  int32_t by_pair;   // a Cut for every pair, else one for every CTA
   float* ws_o;       // [CTAs][2][QR][D]: partial results of the pair that a CTA ends, and of the one that it begins
   float2* ws_ml;     // [CTAs][2][QR]: maximum (log2), sum
-  struct Cut* ws_cut;  // [CTAs]
+  struct Cut* ws_cut;  // [CTAs], of which [pairs] are used where there are fewer
   uint32_t* status;
 };
 
-// The pair that CTA i was the first to find begun: what CTAs first .. last did of it is joined.  pair < 0: none.
+// What CTAs first .. last did of a pair is joined.  pair < 0: nothing (a pair that one CTA had whole, or a CTA that
+// left no pair begun).
 struct alignas(16) Cut {
   int32_t pair, first, last, n_new;
   int64_t row0;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
       runs[0] = min(total, blockIdx.x * run);
       runs[1] = min(total, runs[0] + run);
       runs[2] = run;
-      p.ws_cut[blockIdx.x].pair = -1;
+      if (!p.by_pair) p.ws_cut[blockIdx.x].pair = -1;
     }
     __syncthreads();
   }
@@ -236,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
             const int32_t to = end - at < whole - from ? from + (int32_t)(end - at) : whole;
             found = {q, b, pair, max(0, from - kStart), max(0, to - kStart), units};
             const unsigned long long start = at - from + kStart;  // of the pair's first unit
-            if (from > kStart && start / run + 1 == blockIdx.x)
-              p.ws_cut[blockIdx.x] = {pair, (int)blockIdx.x - 1, (int)((start + units - 1) / run), q.n_new, q.row0, 0};
+            if (found.begin == 0 && found.end > 0 && (found.end < units || p.by_pair))  // begun here
+              p.ws_cut[p.by_pair ? b * (c.kv_heads * p.qtiles) + pair : (int)blockIdx.x] = {
+                  found.end < units ? pair : -1, (int)blockIdx.x, (int)((start + units - 1) / run), q.n_new, q.row0, 0};
             step = to - from;
             break;
           }
@@ -667,53 +670,83 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
   }
 }
 
-// The parts of the pairs that CTAs' ends cut, added in their order.  CTA (i, row): the row of the pair that CTA i
-// of the main kernel was the first to find begun; its warps take the parts in turn, four at a time in flight.
-template <int DIM>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int D = 2 * DIM;
-  __shared__ float os[kWarps][D];
-  __shared__ float ls[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y, qr = gridDim.y;
+// The parts of the pairs that CTAs' ends cut, added in a fixed order.  CTA (i, row): a row of pair i, or of the pair
+// that CTA i of the main kernel left begun, whichever are fewer (blocks with nothing to do cost: 8 pairs in 444 CTAs
+// 45.2 us, as 8 blocks a row 41.3).  Its warps take the parts in turn, four at a time in flight (a pair of 131072 keys has 56).
+template <int DIM, int W>
+__global__ void __launch_bounds__(W * 32) kv4_join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int D = 2 * DIM, V = D / 64;
+  __shared__ float os[W][D];
+  __shared__ float2 mls[W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, qr = gridDim.y, row = blockIdx.y;
   follow();  // the main kernel's results
   const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.ws_cut + blockIdx.x));  // pair, first, last, n_new
-  const longlong2 cut2 = __ldcg(reinterpret_cast<const longlong2*>(p.ws_cut + blockIdx.x) + 1);
+  if (p.by_pair) {  // pairs that a sequence does not have are not written
+    const int of_seq = p.c.kv_heads * p.qtiles;
+    const Kv4Seq q = kv4_seq(p.c, (int)blockIdx.x / of_seq);
+    if ((int)blockIdx.x % of_seq >= (q.n_new * p.shared + qr - 1) / qr * p.c.kv_heads) return;
+  }
   if (cut.x < 0) return;
+  const longlong2 cut2 = __ldcg(reinterpret_cast<const longlong2*>(p.ws_cut + blockIdx.x) + 1);
   const int rows = cut.w * p.shared, qtiles = (rows + qr - 1) / qr;
   const int kvh = cut.x / qtiles, rr = cut.x % qtiles * qr + row;
   if (rr >= rows) return;
   // part s: what CTA first + s did of the pair; the first began it, the others found it begun
   const int parts = cut.z - cut.y + 1;
   auto place = [&](int s) { return ((int64_t)(cut.y + s) * 2 + (s == 0)) * qr + row; };
-  float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, __ldcg(p.ws_ml + place(s)).x);
+  float M = -INFINITY, l = 0.0f;
+  float2 o[V] = {};
+  for (int s0 = warp; s0 < parts; s0 += 4 * W) {
+    float2 ml[4], v[4][V];
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ms = M == -INFINITY ? 0.0f : M;
-  float l = 0.0f;
-  float2 o[D / 64] = {};
-#pragma unroll 4
-  for (int s = warp; s < parts; s += kWarps) {
-    const float2 ml = __ldcg(p.ws_ml + place(s));
-    const float f = ex2(ml.x - ms);
-    l += f * ml.y;
+    for (int k = 0; k < 4; ++k) {
+      const int s = s0 + k * W;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      if (s < parts) ml[k] = __ldcg(p.ws_ml + place(s));
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws_o + place(s) * D + i * 64 + lane * 2));
-      o[i].x += f * v.x;
-      o[i].y += f * v.y;
+      for (int i = 0; i < V; ++i) {
+        v[k][i] = make_float2(0.0f, 0.0f);
+        if (s < parts) v[k][i] = __ldcg(reinterpret_cast<const float2*>(p.ws_o + place(s) * D + i * 64 + lane * 2));
+      }
+    }
+    const float top = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+    const float ms = top == -INFINITY ? 0.0f : top, f0 = ex2(M - ms);
+    M = top;
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i].x *= f0, o[i].y *= f0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = ex2(ml[k].x - ms);
+      l = fmaf(f, ml[k].y, l);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        o[i].x = fmaf(f, v[k][i].x, o[i].x);
+        o[i].y = fmaf(f, v[k][i].y, o[i].y);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) *reinterpret_cast<float2*>(&os[warp][i * 64 + lane * 2]) = o[i];
-  if (lane == 0) ls[warp] = l;
+  for (int i = 0; i < V; ++i) *reinterpret_cast<float2*>(&os[warp][i * 64 + lane * 2]) = o[i];
+  if (lane == 0) mls[warp] = make_float2(M, l);
   __syncthreads();
   if (threadIdx.x >= D / 2) return;
   const int d = threadIdx.x * 2;
-  l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < W; ++w) M = fmaxf(M, mls[w].x);
+  const float ms = M == -INFINITY ? 0.0f : M;
+  float o0 = 0.0f, o1 = 0.0f;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const float f = ex2(mls[w].x - ms);
+    const float2 v = *reinterpret_cast<const float2*>(&os[w][d]);
+    l = fmaf(f, mls[w].y, l);
+    o0 = fmaf(f, v.x, o0);
+    o1 = fmaf(f, v.y, o1);
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const float o0 = (os[0][d] + os[1][d]) + (os[2][d] + os[3][d]);
-  const float o1 = (os[0][d + 1] + os[1][d + 1]) + (os[2][d + 1] + os[3][d + 1]);
   const int tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
   *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (cut2.x + tok) * p.ldo + head * DIM + d % DIM) =
       pack_bf16(o0 * inv, o1 * inv);
@@ -721,6 +754,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const __grid_constan
 
 struct Plan {
   int nt, qtiles, cluster, ctas;  // ctas: of the counted form, 0 for a cluster per pair
+  int cuts;                       // pairs or CTAs, the fewer
 };
 
 // Tiles of 8 query rows where there are more than 4.  A cluster per pair, as large as the places on the GPU allow,
@@ -737,6 +771,7 @@ Plan plan(const ifq_kv4_cache& c, int shared) {
   while (r.cluster < kMaxCluster && pairs * r.cluster * 2 <= places && r.cluster * kWarps < units) r.cluster *= 2;
   r.ctas = c.B <= kMaxSeqs && (units > r.cluster * kWarps * 8 || pairs > places) ? (int)places : 0;
   if (r.ctas) r.cluster = 1;
+  r.cuts = (int)(pairs < r.ctas ? pairs : r.ctas);
   return r;
 }
 
@@ -771,7 +806,10 @@ template <int DIM>
 cudaError_t launch(const AttnParams& p, const Plan& r, cudaStream_t s) {
   cudaError_t e = r.nt == 1 ? launch_nt<DIM, 1>(p, s) : launch_nt<DIM, 2>(p, s);
   if (e != cudaSuccess || !r.ctas) return e;
-  return launch_following<AttnParams>(kv4_join_kernel<DIM>, dim3((unsigned)r.ctas, 4u * r.nt), kThreads, 0, 1, p, s);
+  // few pairs have many parts each: 8 pairs 40.0 us with 8 warps a row, 41.3 with 4; 128 pairs 41.6 against 40.1
+  const dim3 grid((unsigned)r.cuts, 4u * r.nt);
+  if (r.cuts <= 32) return launch_following<AttnParams>(kv4_join_kernel<DIM, 8>, grid, 256, 0, 1, p, s);
+  return launch_following<AttnParams>(kv4_join_kernel<DIM, 4>, grid, 128, 0, 1, p, s);
 }
 
 }  // namespace
@@ -797,6 +835,7 @@ cudaError_t launch_kv4_attention(const ifq_kv4_cache& c, int shared, const float
   p.shared = shared;
   p.cluster = r.cluster;
   p.counted = r.ctas;
+  p.by_pair = r.cuts < r.ctas;
   p.qtiles = r.qtiles;
   p.ws_cut = static_cast<Cut*>(ws);
   p.ws_o = reinterpret_cast<float*>(p.ws_cut + r.ctas);

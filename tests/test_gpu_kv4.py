@@ -372,6 +372,24 @@ def test_attention_scale_not_finite(scale):
         assert torch.isnan(x[:2]).all() and (x[2:] == 77.0).all()
 
 
+@pytest.mark.parametrize("lens,news,heads,shared,dim", [
+    ([9000, 5003, 37, 0], [16, 3, 0, 0], 2, 3, 64), ([20001], [5], 1, 8, 32), ([3000, 9001, 1], [1, 16, 1], 3, 5, 128),
+    ([700] * 60 + [9000], [1] * 60 + [2], 8, 8, 64), ([1] * 30 + [12000] + [40] * 30, [1] * 61, 8, 1, 64)])
+def test_attention_cut_pairs(lens, news, heads, shared, dim):
+    """Runs that cut pairs, where sequences have fewer tiles of rows than the call allows for; fewer and more pairs than
+    blocks."""
+    c = Case(lens, news, heads, dim, 64, seed=len(lens) + dim, n_new=16 if len(lens) < 5 else None)
+    c.fill_random()
+    assert Q.ifq_kv4_attention_workspace_bytes(c.cache, heads * shared) > 0
+    c.attention(shared)
+    torch.cuda.synchronize()
+    c.check(shared)
+    first = [x.clone() for x in c.o]
+    c.attention(shared, q=c.q)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, c.o))
+
+
 @pytest.mark.parametrize("B", [1024, 1025])
 def test_attention_most_sequences_that_are_counted(B):
     """The most sequences whose runs are counted, and one more: a block per pair whatever the lengths."""
