@@ -51,6 +51,7 @@ struct Item {
 
 // Record `tile` (counted from the first that the new tokens touch) of head `head` of sequence blockIdx.z.
 IFQ_DEVINL bool find_item(const AppendParams& p, const Kv4Seq& q, int32_t tile, int head, Item* it) {
+  if (q.n_new == 0) return false;  // its last record holds no token of the call: its page is not looked up
   it->q = q;
   it->head = head;
   // a sequence whose length is unusable has no positions, but its rows still read as 0

@@ -657,3 +657,32 @@ def test_decode_steps_through_the_library():
         y = torch.cat([out["y_re"], out["y_im"]], dim=1).double().cpu().numpy()
         assert np.all(np.abs(y - ov @ Wv.T) <= 32 * 2.0 ** -22 * (np.abs(ov) @ np.abs(Wv).T))
     assert int(st) == 0
+
+
+# ------------------------------------------------------------------ what a call does not name
+@pytest.mark.parametrize("n_new", [1, 8, 16, 32])
+def test_idle_sequence_names_no_page(n_new):
+    """A sequence without new tokens whose length ends inside a record of a page that was given back (-1): nothing of
+    the call names that page, so no form of it reports a range, and the other sequence's tokens are written."""
+    c = Case([37, 5 + n_new, 16], [0, n_new, 0], 3, 64, 16, seed=50 + n_new)
+    c.fill_random()
+    c.table[0, 2] = -1                               # the page of tokens 32..36
+    c.d_table.copy_(to_dev(c.table))
+    planes = c.planes()
+    st = status_word()
+    Q.ifq_kv4_append(c.cache, *[to_dev(x) for x in planes], dev_status=st)
+    out = [torch.full((c.rows, 3 * 64), 55.0, device=DEV) for _ in range(4)]
+    Q.ifq_kv4_read(c.cache, *out, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    c.put(planes)
+    np.testing.assert_array_equal(c.d_records.cpu().numpy(), c.records)
+    for x, o in zip(planes, out):
+        n, s, m = F.kv4_quantize(x[:c.used].reshape(c.used, 3, 64))
+        np.testing.assert_array_equal(o.cpu().numpy()[:c.used], F.kv4_values(n, s, m).astype(np.float32).reshape(c.used, -1))
+        assert torch.all(o[c.used:] == 55.0)
+    if n_new <= Q.IFQ_KV4_MAX_NEW:
+        c.attention(2, status=st)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        c.check(2, skip=(0,))
