@@ -71,11 +71,10 @@ struct AttnParams {
 };
 
 // What CTAs first .. last did of a pair is joined.  pair < 0: nothing (a pair that one CTA had whole, or a CTA that
-// left no pair begun).
+// left no pair begun).  Read 16 bytes at a time.
 struct alignas(16) Cut {
   int32_t pair, first, last, n_new;
   int64_t row0;
-  int64_t unused;
 };
 
 IFQ_DEVINL float ex2(float x) {
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
             const unsigned long long start = at - from + kStart;  // of the pair's first unit
             if (found.begin == 0 && found.end > 0 && (found.end < units || p.by_pair))  // begun here
               p.ws_cut[p.by_pair ? b * (c.kv_heads * p.qtiles) + pair : (int)blockIdx.x] = {
-                  found.end < units ? pair : -1, (int)blockIdx.x, (int)((start + units - 1) / run), q.n_new, q.row0, 0};
+                  found.end < units ? pair : -1, (int)blockIdx.x, (int)((start + units - 1) / run), q.n_new, q.row0};
             step = to - from;
             break;
           }
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
       const int32_t tl = base + lane;
       if (tl >= t_end) return 0xFFFFFFFFu;
       const int32_t pc = (int32_t)((uint32_t)tl / (uint32_t)c.page_tiles), in = tl - pc * c.page_tiles;
-      const int32_t page = __ldg(c.page_table + (int64_t)b * c.table_cols + pc);
+      const int32_t page = ld_after(c.page_table + (int64_t)b * c.table_cols + pc);
       if (page < 0 || page >= c.pages) {
         set_status(p.status, IFQ_DEV_RANGE);
         return 0xFFFFFFFFu;
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
         const float* src = p.q[lane / 16] + (sq.row0 + tok) * p.ldq + head * DIM + lane % 16 * E;
 #pragma unroll
         for (int j = 0; j < E; j += 2) {
-          const float2 x = __ldg(reinterpret_cast<const float2*>(src + j));
+          const float2 x = ld_after(reinterpret_cast<const float2*>(src + j));
           v[j] = x.x;
           v[j + 1] = x.y;
         }
@@ -680,14 +679,14 @@ __global__ void __launch_bounds__(W * 32) kv4_join_kernel(const __grid_constant_
   __shared__ float2 mls[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, qr = gridDim.y, row = blockIdx.y;
   follow();  // the main kernel's results
-  const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.ws_cut + blockIdx.x));  // pair, first, last, n_new
+  const int4 cut = ld_after(reinterpret_cast<const int4*>(p.ws_cut + blockIdx.x));  // pair, first, last, n_new
   if (p.by_pair) {  // pairs that a sequence does not have are not written
     const int of_seq = p.c.kv_heads * p.qtiles;
     const Kv4Seq q = kv4_seq(p.c, (int)blockIdx.x / of_seq);
     if ((int)blockIdx.x % of_seq >= (q.n_new * p.shared + qr - 1) / qr * p.c.kv_heads) return;
   }
   if (cut.x < 0) return;
-  const longlong2 cut2 = __ldcg(reinterpret_cast<const longlong2*>(p.ws_cut + blockIdx.x) + 1);
+  const int64_t row0 = ld_after(&p.ws_cut[blockIdx.x].row0);
   const int rows = cut.w * p.shared, qtiles = (rows + qr - 1) / qr;
   const int kvh = cut.x / qtiles, rr = cut.x % qtiles * qr + row;
   if (rr >= rows) return;
@@ -702,11 +701,11 @@ __global__ void __launch_bounds__(W * 32) kv4_join_kernel(const __grid_constant_
     for (int k = 0; k < 4; ++k) {
       const int s = s0 + k * W;
       ml[k] = make_float2(-INFINITY, 0.0f);
-      if (s < parts) ml[k] = __ldcg(p.ws_ml + place(s));
+      if (s < parts) ml[k] = ld_after(p.ws_ml + place(s));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         v[k][i] = make_float2(0.0f, 0.0f);
-        if (s < parts) v[k][i] = __ldcg(reinterpret_cast<const float2*>(p.ws_o + place(s) * D + i * 64 + lane * 2));
+        if (s < parts) v[k][i] = ld_after(reinterpret_cast<const float2*>(p.ws_o + place(s) * D + i * 64 + lane * 2));
       }
     }
     const float top = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
@@ -748,7 +747,7 @@ __global__ void __launch_bounds__(W * 32) kv4_join_kernel(const __grid_constant_
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int tok = rr / p.shared, head = kvh * p.shared + rr % p.shared;
-  *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (cut2.x + tok) * p.ldo + head * DIM + d % DIM) =
+  *reinterpret_cast<uint32_t*>(p.o[d / DIM] + (row0 + tok) * p.ldo + head * DIM + d % DIM) =
       pack_bf16(o0 * inv, o1 * inv);
 }
 

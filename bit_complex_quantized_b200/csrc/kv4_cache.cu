@@ -117,6 +117,7 @@ IFQ_DEVINL uint32_t key_word(const float4& a, const float4& b, const Group& q) {
   return codes_of(make_float4(a.x, a.z, b.x, b.z), q) | (codes_of(make_float4(a.y, a.w, b.y, b.w), q) << 16);
 }
 
+// src: from behind_wait.
 IFQ_DEVINL float4 take(const float* src, bool in) {
   return in ? __ldcs(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_tokens_kernel(const __gri
   const int32_t pos = q.len - q.n_new + tok;
   uint8_t* rec = live ? kv4_record(c, b, head, pos >> 4) : nullptr;
   float4 x[2];
-  const float* src = p.src[plane] + (q.row0 + tok) * p.ld + head * DIM + part * 8;
+  const float* src = behind_wait(p.src[plane]) + (q.row0 + tok) * p.ld + head * DIM + part * 8;
   x[0] = take(src, live);
   x[1] = take(src + 4, live);
   float lo = INFINITY, hi = -INFINITY;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, records_ctas(DIM))
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, plane = threadIdx.x >> 5, pl = plane & 1;
   const int32_t len = it.q.len;
   auto in = [&](int r) { return it.pos0 + r >= it.first && it.pos0 + r < len; };
-  const float* src = p.src[plane] + (it.q.row0 + it.pos0 - it.first) * p.ld + it.head * DIM;
+  const float* src = behind_wait(p.src[plane]) + (it.q.row0 + it.pos0 - it.first) * p.ld + it.head * DIM;
   const bool all = in(0) && in(15);
   bool bad = false;
   const int heads = min(p.heads_each, p.c.kv_heads - it.head);

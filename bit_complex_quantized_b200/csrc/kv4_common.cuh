@@ -54,10 +54,11 @@ struct Kv4Seq {
 IFQ_DEVINL Kv4Seq kv4_seq(const Kv4Arg& c, int b) {
   Kv4Seq s;
   s.ok = true;
+  s.len = ld_after(c.kv_lens + b);
   s.row0 = (int64_t)b * c.n_new;
   s.n_new = c.n_new;
   if (c.new_offsets) {
-    const int32_t o0 = __ldg(c.new_offsets + b), o1 = __ldg(c.new_offsets + b + 1);
+    const int32_t o0 = ld_after(c.new_offsets + b), o1 = ld_after(c.new_offsets + b + 1);
     s.row0 = o0;
     s.n_new = o1 - o0;
     if (o0 < 0 || o1 < o0 || o1 > c.rows || s.n_new > c.n_new) {
@@ -65,7 +66,6 @@ IFQ_DEVINL Kv4Seq kv4_seq(const Kv4Arg& c, int b) {
       s.n_new = 0;
     }
   }
-  s.len = __ldg(c.kv_lens + b);
   if (s.len < s.n_new || s.len > c.table_cols * c.page_tiles * 16) s.ok = false;
   if (!s.ok) s.len = 0;
   return s;
@@ -75,7 +75,7 @@ IFQ_DEVINL Kv4Seq kv4_seq(const Kv4Arg& c, int b) {
 // table does not name a page of the cache.
 IFQ_DEVINL uint8_t* kv4_record(const Kv4Arg& c, int b, int h, int32_t tile) {
   const int32_t pc = tile / c.page_tiles, in = tile - pc * c.page_tiles;
-  const int32_t page = __ldg(c.page_table + (int64_t)b * c.table_cols + pc);
+  const int32_t page = ld_after(c.page_table + (int64_t)b * c.table_cols + pc);
   if (page < 0 || page >= c.pages) return nullptr;
   return c.records + (((int64_t)page * c.kv_heads + h) * c.page_tiles + in) * c.record_bytes;
 }

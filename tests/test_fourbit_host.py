@@ -1,6 +1,7 @@
 """Host-side checks of the 4-bit layers and cache (no GPU needed): argument errors come back as status codes or
 ValueError before any CUDA call, and the oracle's layout and quantizer hold their definitions."""
 import ctypes
+import os
 from fractions import Fraction
 
 import numpy as np
@@ -212,3 +213,19 @@ def test_quantizers_round_exact_quotients():
         sv, mv = (Fraction(float(F.bf16_value(t[r:r + 1])[0])) for t in (s, m))
         for k in range(64):
             assert n[r, k] == max(0, min(15, _half_even((Fraction(float(x[r, k])) - mv) / sv)))
+
+
+# ------------------------------------------------------------------ kernels that are launched while the one before ends
+def test_kernels_that_follow_read_behind_their_wait():
+    """A kernel that starts before the one in front of it has ended reads nothing through the read-only path, whose
+    lines may be older than its wait, nor by loads that the compiler may move in front of the wait."""
+    csrc = os.path.dirname(L.__file__) + "/csrc/"
+    found = 0
+    for name in sorted(os.listdir(csrc)):
+        text = open(csrc + name).read()
+        if "follow();" in text or name == "kv4_common.cuh":
+            found += 1
+            for load in ("__ldg(", "__ldcg(", "__ldca(", "ldg_stream(", "ld.global.nc"):
+                assert load not in text, (name, load)
+            assert "__ldcs(" not in text or "behind_wait(" in text
+    assert found == 4                                 # w4_gemv, kv4_cache, kv4_attention and what the last two share
