@@ -49,6 +49,7 @@ constexpr int kUnit = 32;                  // keys of a warp's step: two records
 constexpr int kStages = 2;
 constexpr int kSlack = 6;                  // how far (log2) a score may pass the reference
 constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxSeqs = 8 * kThreads;     // sequences that a CTA counts, up to 8 a thread
 
 // CTAs that an SM holds (its registers decide).
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (mx > 0x1p100f) {  // its scores would overflow: the row counts as not finite
+      if (mx > 0x1p99f * kLog2e) {  // |scale q| above 2^99, whose scores could overflow: the row counts as not finite
         bad = true;
         v[0] = NAN;
       }
@@ -830,7 +831,7 @@ cudaError_t launch_kv4_attention(const ifq_kv4_cache& c, int shared, const float
   p.o[1] = o_im;
   p.ldq = ldq;
   p.ldo = ldo;
-  p.scale2 = scale * 1.4426950408889634f;
+  p.scale2 = scale * kLog2e;
   p.shared = shared;
   p.cluster = r.cluster;
   p.counted = r.ctas;

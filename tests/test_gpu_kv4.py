@@ -686,3 +686,28 @@ def test_idle_sequence_names_no_page(n_new):
         torch.cuda.synchronize()
         assert int(st) == 0
         c.check(2, skip=(0,))
+
+
+# ------------------------------------------------------------------ limits as documented
+@pytest.mark.parametrize("scale", [1.0, 0.0625, -2.0])
+def test_attention_query_limit(scale):
+    """|scale q| of 2^99 is taken, the next float above it counts as not finite (the powers of two of the scale are
+    exact, so nothing is rounded on the way there but the factor log2 e, which keeps the order)."""
+    c = Case([40, 40, 40], [1, 1, 1], 1, 64, 16, seed=60)
+    c.fill_random(spread=2.0 ** -90)                 # keys near 2^-90: scores of order 2^9
+    q = [np.zeros((c.rows, 64), np.float32) for _ in range(2)]
+    top = np.float32(2.0 ** 99 / abs(scale))
+    q[0][0, 3], q[1][1, 7], q[1][2, 7] = top, np.nextafter(top, np.float32(np.inf)), -1.3 * top
+    st = status_word()
+    c.attention(1, q=q, scale=scale, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == Q.IFQ_DEV_NONFINITE
+    for x in c.o:
+        assert torch.isfinite(x[0]).all() and torch.isnan(x[1:3]).all()
+    q[1][1:3] = 0
+    st.zero_()
+    c.attention(1, q=q, scale=scale, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    c.check(1, skip=(0,))
+    assert all(torch.isfinite(x[0]).all() for x in c.o)
