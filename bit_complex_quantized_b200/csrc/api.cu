@@ -367,6 +367,7 @@ ifq_status check_kv4(const ifq_kv4_cache* c) {
   if (c->pages < 1 || c->pages > 0x7FFFFFFF || c->page_tokens < 16 || c->page_tokens > 65536 || c->page_tokens % 16)
     return IFQ_ERR_SHAPE;
   if (c->kv_heads < 1 || c->kv_heads > 1024 || (c->dim != 32 && c->dim != 64 && c->dim != 128)) return IFQ_ERR_SHAPE;
+  if (c->pages * c->kv_heads * (c->page_tokens / 16) > 0xFFFFFFFFll) return IFQ_ERR_SHAPE;  // record numbers are 32-bit
   if (c->B < 1 || c->B > 65535 || c->table_cols < 1 || c->table_cols > (int64_t)1 << 26) return IFQ_ERR_SHAPE;
   // positions are 32-bit
   if (c->table_cols * c->page_tokens > ((int64_t)1 << 31) - 65536) return IFQ_ERR_SHAPE;

@@ -522,7 +522,7 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *               n_new rows each (launches are sized by n_new: give the most that a
  *               sequence has, not more).  rows: allocated rows of those buffers; rows that
  *               belong to no sequence are neither read nor written.
- *   pages 1..2^31-1     page_tokens  a multiple of 16, 16..65536
+ *   pages 1..2^31-1, at most 2^32 - 1 records     page_tokens  a multiple of 16, 16..65536
  *   kv_heads 1..1024    B 1..65535    n_new >= 1    table_cols 1..2^26, at most
  *   2^31 - 65536 positions (table_cols * page_tokens)    rows 1..2^31-1
  * page_table, kv_lens and new_offsets are device memory, read when the call's

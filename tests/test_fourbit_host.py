@@ -229,3 +229,17 @@ def test_kernels_that_follow_read_behind_their_wait():
                 assert load not in text, (name, load)
             assert "__ldcs(" not in text or "behind_wait(" in text
     assert found == 4                                 # w4_gemv, kv4_cache, kv4_attention and what the last two share
+
+
+# ------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("kw", [dict(pages=1 << 30, kv_heads=4), dict(pages=1 << 20, kv_heads=1024, page_tokens=65536),
+                                dict(pages=(1 << 32) // 16, page_tokens=64, kv_heads=4)])
+def test_cache_of_more_records_than_are_counted(kw):
+    """Attention numbers records in 32 bits, and the last number is none."""
+    c = _cache(**kw)
+    width = c.kv_heads * 64
+    assert c.pages * c.kv_heads * (c.page_tokens // 16) >= 1 << 32
+    assert _append(c, ld=width) == SHAPE and _attend(c, heads=c.kv_heads, ldq=width, ldo=width) == SHAPE
+    assert Q.load().ifq_kv4_attention_workspace_bytes(ctypes.byref(c), c.kv_heads) == 0
+    c.pages = ((1 << 32) - 1) // (c.kv_heads * (c.page_tokens // 16))
+    assert _append(c, ld=width) != SHAPE and _attend(c, heads=c.kv_heads, ldq=width, ldo=width) != SHAPE
