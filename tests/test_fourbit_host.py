@@ -241,5 +241,8 @@ def test_cache_of_more_records_than_are_counted(kw):
     assert c.pages * c.kv_heads * (c.page_tokens // 16) >= 1 << 32
     assert _append(c, ld=width) == SHAPE and _attend(c, heads=c.kv_heads, ldq=width, ldo=width) == SHAPE
     assert Q.load().ifq_kv4_attention_workspace_bytes(ctypes.byref(c), c.kv_heads) == 0
+    # one page fewer is taken (a missing workspace is refused after the sizes: nothing is launched)
     c.pages = ((1 << 32) - 1) // (c.kv_heads * (c.page_tokens // 16))
-    assert _append(c, ld=width) != SHAPE and _attend(c, heads=c.kv_heads, ldq=width, ldo=width) != SHAPE
+    c.table_cols = (1 << 20) // c.page_tokens
+    assert Q.load().ifq_kv4_attention_workspace_bytes(ctypes.byref(c), c.kv_heads) > 0
+    assert _attend(c, heads=c.kv_heads, ldq=width, ldo=width, nb=0) == WORKSPACE
