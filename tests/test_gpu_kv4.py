@@ -711,3 +711,32 @@ def test_attention_query_limit(scale):
     assert int(st) == 0
     c.check(1, skip=(0,))
     assert all(torch.isfinite(x[0]).all() for x in c.o)
+
+
+# ------------------------------------------------------------------ two calls at once
+def test_attention_of_two_caches_at_once():
+    """Two caches' calls on two streams, one of them a captured graph, with a workspace each and nothing on the host
+    between them: each has the result that it has alone, over and over."""
+    a, b = Case([20011, 9, 4097], [1, 1, 1], 2, 64, 64, seed=70), Case([9000, 12001], [2, 1], 3, 64, 32, seed=71)
+    for c, shared in ((a, 8), (b, 3)):
+        c.fill_random()
+        c.attention(shared)
+        torch.cuda.synchronize()
+        c.check(shared)
+        c.alone = [x.clone() for x in c.o]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            Q.ifq_kv4_attention(a.cache, *a.d_q, *a.o, scale=a.scale, workspace=a.ws)
+    for _ in range(5):
+        for c in (a, b):
+            c.ws.fill_(0xFF)
+            for x in c.o:
+                x.fill_(77.0)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        for _ in range(4):
+            Q.ifq_kv4_attention(b.cache, *b.d_q, *b.o, scale=b.scale, workspace=b.ws, stream=side)
+        torch.cuda.synchronize()
+        for c in (a, b):
+            assert all(torch.equal(x, y) for x, y in zip(c.alone, c.o))
