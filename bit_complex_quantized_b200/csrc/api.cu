@@ -396,8 +396,7 @@ ifq_status check_kv4_attention(const ifq_kv4_cache* c, int q_heads) {
   if (st != IFQ_OK) return st;
   if (c->n_new > IFQ_KV4_MAX_NEW) return IFQ_ERR_BATCH;
   if (q_heads < c->kv_heads || q_heads % c->kv_heads || q_heads > 4096) return IFQ_ERR_SHAPE;
-  // (key/value head, query tile) is one grid dimension
-  if ((int64_t)c->kv_heads * ((int64_t)c->n_new * (q_heads / c->kv_heads) / 4 + 1) > 65535) return IFQ_ERR_SHAPE;
+  // (key/value head, tile of 4 query rows) is one grid dimension: at most 16 * 4096 / 4 + 1024
   return IFQ_OK;
 }
 

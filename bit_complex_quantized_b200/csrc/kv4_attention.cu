@@ -136,9 +136,6 @@ struct Segment {
 // 16 to 32 65 us; equal lengths hardly change.)
 constexpr int kStart = 24;
 
-IFQ_DEVINL void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 IFQ_DEVINL float2 ld_cluster2(const void* smem, uint32_t rank) {
   uint32_t a;
   float2 v;
@@ -777,18 +774,6 @@ Plan plan(const ifq_kv4_cache& c, int shared) {
 
 // Partial results of the counted form, rows.
 int64_t partials(const Plan& r) { return (int64_t)r.ctas * 2 * 4 * r.nt; }
-
-// The kernel's shared memory above 48 KB has to be allowed once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, uint64_t* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (__atomic_load_n(done, __ATOMIC_ACQUIRE) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) __atomic_fetch_or(done, (uint64_t)1 << dev, __ATOMIC_RELEASE);
-  return e;
-}
 
 template <int DIM, int NT>
 cudaError_t launch_nt(const AttnParams& p, cudaStream_t s) {

@@ -15,11 +15,11 @@
 
 namespace ifq {
 
-constexpr int kQ4TileRows = 16, kQ4TileCols = 64, kQ4TileBytes = 512;
+constexpr int kQ4TileBytes = 512;
 
 // A code n in bits 0-3 of a bf16 is the number n 2^-133 (a subnormal, since exponent fields 0 and 1
 // share one spacing), and in bits 4-7 it is 16 n 2^-133.  One fused multiply-add per register turns
-// both into (n - 8) 2^-6 or n 2^-6 exactly: multiplier 2^127 or 2^123, addend -2^-3 or 0.
+// both into (n - 8) 2^-6 exactly: multiplier 2^127 or 2^123, addend -2^-3.
 constexpr uint32_t kQ4Mul0 = 0x7F007F00u;   // 2^127, twice
 constexpr uint32_t kQ4Mul1 = 0x7D007D00u;   // 2^123
 constexpr uint32_t kQ4Sub8 = 0xBE00BE00u;   // -2^-3 = -8 2^-6
@@ -31,14 +31,13 @@ IFQ_DEVINL uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
-// The four operand registers of a word: (n - 8) 2^-6 where kAdd = kQ4Sub8, n 2^-6 where it is -0.
-template <uint32_t kAdd>
+// The four operand registers of a word: (n - 8) 2^-6.
 IFQ_DEVINL void q4_expand(uint32_t w, uint32_t (&a)[4]) {
   const uint32_t v = w >> 8;
-  a[0] = fma_bf16x2(w & 0x000F000Fu, kQ4Mul0, kAdd);
-  a[1] = fma_bf16x2(w & 0x00F000F0u, kQ4Mul1, kAdd);
-  a[2] = fma_bf16x2(v & 0x000F000Fu, kQ4Mul0, kAdd);
-  a[3] = fma_bf16x2(v & 0x00F000F0u, kQ4Mul1, kAdd);
+  a[0] = fma_bf16x2(w & 0x000F000Fu, kQ4Mul0, kQ4Sub8);
+  a[1] = fma_bf16x2(w & 0x00F000F0u, kQ4Mul1, kQ4Sub8);
+  a[2] = fma_bf16x2(v & 0x000F000Fu, kQ4Mul0, kQ4Sub8);
+  a[3] = fma_bf16x2(v & 0x00F000F0u, kQ4Mul1, kQ4Sub8);
 }
 
 // D += A B, m16n8k16, bf16 operands, float32 accumulators.
@@ -233,6 +232,23 @@ cudaError_t launch_following(void (*kernel)(P), dim3 grid, int threads, int smem
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// A kernel's shared memory above 48 KB has to be allowed once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, uint64_t* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (__atomic_load_n(done, __ATOMIC_ACQUIRE) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) __atomic_fetch_or(done, (uint64_t)1 << dev, __ATOMIC_RELEASE);
+  return e;
+}
+
+// Everything that the cluster's CTAs did before is seen by all of them behind it.
+IFQ_DEVINL void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // 16 bytes that are read once, past L1.

@@ -85,9 +85,6 @@ IFQ_DEVINL uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-IFQ_DEVINL void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 IFQ_DEVINL float ld_cluster(const void* smem, uint32_t rank) {
   uint32_t a;
   float v;
@@ -201,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas))
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t lo[4], hi[4];
-        q4_expand<kQ4Sub8>(c ? w4.z : w4.x, lo);
-        q4_expand<kQ4Sub8>(c ? w4.w : w4.y, hi);
+        q4_expand(c ? w4.z : w4.x, lo);
+        q4_expand(c ? w4.w : w4.y, hi);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if (c == 0 || G == 32) mma_bf16_first(part[nt], lo[0], hi[0], lo[1], hi[1], b[c][nt].x, b[c][nt].y);
@@ -285,18 +282,6 @@ __global__ void __launch_bounds__(kThreads, (Ring<G, XB>::kCtas))
   }
   if (bad) set_status(p.status, IFQ_DEV_NONFINITE);
   if (p.cluster > 1) cluster_sync();  // no CTA leaves while its sums are being read
-}
-
-// The kernel's shared memory above 48 KB has to be allowed once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, uint64_t* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (__atomic_load_n(done, __ATOMIC_ACQUIRE) >> dev & 1)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) __atomic_fetch_or(done, (uint64_t)1 << dev, __ATOMIC_RELEASE);
-  return e;
 }
 
 // When the CTAs of a launch end: the places on the GPU by the time at which each is free.
