@@ -31,10 +31,23 @@
 //               parts each 79 us).
 // All joins add in a fixed order.
 //
-// Bound: 131072 tokens of 8 heads (64 query heads, 151 MB) take 41 us.  About 15 us of that do not grow with the length:
-// two launches, counting, a pair's q and first copies, the joins.  Each further 131072 tokens take 26 us (89 % of the
-// copy rate); the loop's arithmetic alone takes as long: 280 warp instructions per record and pair of 8 rows (80 to unmask
-// codes, 24 matrix instructions, 60 for scores and weights) at half the issue rate.
+// Every pair is a pass of its own over its head's records: query rows beyond 8 (new tokens times shared heads) cost
+// another pass each 8 (8 sequences of 20000 tokens, 8 heads, 8 query heads each: 1 new token 47 us, 4 148 us, 16 542 us).
+//
+// The form is chosen on the host by the positions that the page table has room for, not by the lengths, which are on the
+// device: 777 tokens of 32 heads in a table of 131072 positions take the counted form, 11.4 us instead of 6.4.
+//
+// Rounding: the weights enter the second product as one fp16 term.  The output is bf16, whose rounding is 8 times
+// coarser; with a second term the error against 64 bits goes from 1.73 to 1.72 10^-3 (131072 tokens) and the time from 50.0
+// to 51.8 us, for 32 ragged sequences from 74.7 to 80.9 us (L2 flushed).  q needs two: the absolute error of a score is
+// the relative one of its weight, and scores are large.
+//
+// Bound: 131072 tokens of 8 heads (64 query heads, 151 MB) take 41 us (captured, caches that L2 does not hold).  About 14
+// us of that do not grow with the length: two launches, counting, a pair's q and first copies, the joins.  Each further
+// 131072 tokens take 27 us, 87 % of the copy rate: 288 warp instructions per record and pair of 8 rows (80 to unmask codes,
+// 24 matrix instructions, 60 for scores and weights), issued at 60 % of the slots.  In all it is bound by latency: 11 warps
+// an SM, whose chains of products, scores and weights keep issue at 48 % and no pipe above 44 %.  The registers spilled for
+// 8 rows at dim 64 are read 6 times a warp, outside the loop over the records.
 #include "ifq_internal.h"
 #include "kv4_common.cuh"
 

@@ -5,21 +5,25 @@
 // (q4_common.cuh), x is the B operand as it is, so all products are exact and a group accumulates
 // in float32; the group's scale multiplies that sum in float32.
 //
-// HBM-bound by the codes.  A CTA of 4 warps takes 64 rows x a slice of the columns; its warps take
-// 128-column stages of the slice in turn, each for all 64 rows, so that a tile's x is read from
-// shared memory once for all strips, and every warp runs its own ring of asynchronous copies (codes,
-// scales and x of a stage) without a barrier of the CTA.
+// HBM-bound by the codes.  A CTA of 4 warps takes row tiles x a slice of the columns, in stages of 128 columns.  A warp
+// takes 64 rows of a stage, so that a tile's x is read from shared memory once for four strips, and runs its own ring of
+// asynchronous copies of codes and scales.
+//   up to 4 tokens  64 rows a CTA: the warps take the slice's stages in turn, each with a ring of x of its own; no barrier
+//                   but the warp's
+//   5 to 16         128 rows a CTA: two warps with different rows take the same stages and share a ring of x, which each
+//                   fills half of.  They meet at a named barrier (one per pair) every stage, when their copies are in:
+//                   behind it both read the stage, and neither has still to read the one that is filled next
 // The warps' sums are added in shared memory at the end, and where a layer has few row tiles its
 // columns are split over a cluster, whose CTAs add theirs through distributed shared memory: one launch,
 // no workspace, a fixed order of sums.
 //
 // Bound: a word takes 5 integer, 4 bf16 and 1 (2 above 8 tokens) matrix instructions and with loads, scales and
-// copies 16 to 20 issue slots, where the copy rate leaves about 22.  One token: a 7B-shaped block (105 MB) 20.9 us,
-// 78 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start and end.  50021 x 4096 in
-// groups of 32, 5 tokens: 25.4 us, 71 % (a group costs 7 instructions per 2 words).  16 tokens: the block 41 us,
-// the layer set 117 us, 59 %: a matrix instruction takes 8 cycles of a quarter SM and does not run beside the FMA pipe
-// (both measured), so a word's 2 products, 4 conversions and 2 scalings fill the 22 cycles in which HBM delivers it, and
-// the 12 to 16 warps an SM whose registers 16 tokens leave room for keep them at 55 to 60 %.
+// copies 16 to 20 issue slots.  Times are of calls captured in one graph, over weights that L2 does not hold.  One token: a
+// 7B-shaped block (105 MB) 20.7 us, 78 % of the copy rate, a 70B-shaped layer set (442 MB) 78 us, 88 %; the rest is start
+// and end.  50021 x 4096 in groups of 32, 5 tokens: 25.4 us, 71 % (a group costs 7 instructions per 2 words).  16 tokens:
+// the block 41 us, the layer set 116 us, 60 %, by latency: a word's expansion, products and scaling follow one another,
+// and the registers leave 12 to 16 warps an SM to cover that (issue 47 %, tensor pipe 36 %, the first stall a fixed wait).
+// The registers spilled up to 4 tokens are read 21 times a warp in the block, 0.5 % of its instructions.
 #include "ifq_internal.h"
 #include "q4_common.cuh"
 
@@ -338,6 +342,7 @@ cudaError_t launch(const ifq_w4_layer* Ls, int count, int B, uint32_t* dev_statu
     tiles[i] = (Ls[i].rows + R::kRows - 1) / R::kRows;
     longest = stages[i][0] > longest ? stages[i][0] : longest;
   }
+  // (All of it on the host, in every call: 0.2 us for one layer, 0.9 for a block of 7, 43 for 32 layers of 32 widths.)
   // How far to split the columns: to slices of at most `len` stages.  Splitting further helps while CTAs are few or
   // long ones end last, and costs every CTA its start and join (kStart stages' time): of the lengths that some layer
   // can be cut to, the one whose CTAs, started longest first on the GPU's places, end first.

@@ -431,7 +431,8 @@ ifq_status ifq_gemm_wait_limit(const ifq_layer* layers, int count, int T, int64_
  * `rows` in the last tile hold code 8 (zero).  Scales are bf16 bit patterns
  * [ceil(rows/16)][cols/group][16], row r at index 2 (r % 8) + (r % 16) / 8.
  *
- *   rows    1..2^30     cols   a multiple of 64 and of group, <= 2^30
+ *   rows    1..2^30     cols   a multiple of 64 and of group, <= 2^30     rows * cols <= 2^40
+ *   (a call's tiles of 16 x max(64, group) columns: at most 2^31)
  *   group   32, 64 or 128, the same for every tensor or layer of a call
  *   count   1..IFQ_MAX_GROUP tensors or layers
  * Pointers must be 16-byte aligned; another group is IFQ_ERR_SHAPE.
@@ -441,7 +442,8 @@ ifq_status ifq_gemm_wait_limit(const ifq_layer* layers, int count, int T, int64_
  * ifq_w4_dequantize   codes, scales -> w [rows][cols], s q rounded to bf16
  *                     (nearest-even), for the forward pass of
  *                     quantization-aware training and for prefill by a dense
- *                     matrix product.
+ *                     matrix product.  Where max |w| of a group is above 3.38e38,
+ *                     7 s may pass the largest bf16: Inf.
  * ifq_w4_gemv         y = R_hat [x_re; x_im] for B = 1..IFQ_MAX_GEMV_BATCH
  *                     tokens, all layers in one launch.
  *   x_re, x_im   [B][cols/2] bf16 bit patterns; or x_im NULL and x_re [B][cols]
@@ -532,6 +534,7 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  * tokens or more than table_cols * page_tokens counts as empty; a page number
  * outside 0..pages-1 is not touched (appending skips the token, attention
  * leaves its keys out, reading gives 0).  Each sets IFQ_DEV_RANGE.
+ * A sequence without new tokens names no page.
  * Two sequences may share pages that neither appends to; pages that a call
  * appends to must not be shared.
  *
@@ -541,7 +544,8 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  * ifq_kv4_read       the stored values of the same tokens, as float32 (s n + m
  *                    rounded once): what attention uses.
  * ifq_kv4_attention  q_re, q_im [rows][q_heads dim] float32, rows ldq apart, head h
- *                    reading key/value head h / (q_heads / kv_heads); new token i of a
+ *                    reading key/value head h / (q_heads / kv_heads) (q_heads a
+ *                    multiple of kv_heads, <= 4096); new token i of a
  *                    sequence sees positions 0 .. len - n + i (itself included,
  *                    so append first).  o_re, o_im [rows][q_heads dim] bf16, rows
  *                    ldo apart.  score = scale Re(q^T conj(k)).  n_new <=
@@ -551,13 +555,16 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *                    that is more); sums and the softmax's maximum and sum are float32, and
  *                    stay finite for stored values up to 2^100 and scores up to 2^126; partial
  *                    results are joined in a fixed order (bit-reproducible).  A NaN or Inf in q
- *                    or scale, or an entry with |scale q| above 2^99, sets IFQ_DEV_NONFINITE
- *                    and makes that row NaN.
+ *                    or scale, or an entry with |scale q| above 2^99 (to float32 rounding),
+ *                    sets IFQ_DEV_NONFINITE and makes that row NaN.
+ *                    One pass over the cache for every 8 rows of (new token, query head)
+ *                    of a key/value head.  A table with room for many more positions than
+ *                    a few thousand costs short sequences some microseconds.
  *   workspace        device scratch of ifq_kv4_attention_workspace_bytes() bytes,
  *                    16-byte aligned, no initial contents needed; calls that share it
  *                    must not overlap on the GPU.  May be NULL when that is 0.
- * Strides are multiples of 4 elements (o: 2) and at least the row's width, else
- * IFQ_ERR_SHAPE; q, k, v pointers and records are 16-byte aligned, o 4-byte.
+ * Strides are multiples of 4 elements (o: 2), at least the row's width and at most
+ * 2^30, else IFQ_ERR_SHAPE; q, k, v pointers and records are 16-byte aligned, o 4-byte.
  * n_new outside its range is IFQ_ERR_BATCH.  dev_status may be NULL.
  * ------------------------------------------------------------------------- */
 #define IFQ_KV4_MAX_NEW 16
