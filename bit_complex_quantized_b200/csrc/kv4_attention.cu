@@ -829,7 +829,7 @@ cudaError_t launch_kv4_attention(const ifq_kv4_cache& c, int shared, const float
   p.o[1] = o_im;
   p.ldq = ldq;
   p.ldo = ldo;
-  p.scale2 = scale * kLog2e;
+  p.scale2 = fabsf(scale) <= 0x1p127f ? scale * kLog2e : NAN;
   p.shared = shared;
   p.cluster = r.cluster;
   p.counted = r.ctas;

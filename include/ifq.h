@@ -555,8 +555,8 @@ ifq_status ifq_w4_gemv(const ifq_w4_layer* layers, int count, int group, int B, 
  *                    that is more); sums and the softmax's maximum and sum are float32, and
  *                    stay finite for stored values up to 2^100 and scores up to 2^126; partial
  *                    results are joined in a fixed order (bit-reproducible).  A NaN or Inf in q
- *                    or scale, or an entry with |scale q| above 2^99 (to float32 rounding),
- *                    sets IFQ_DEV_NONFINITE and makes that row NaN.
+ *                    or scale, an entry with |scale q| above 2^99 (to float32 rounding), or
+ *                    |scale| above 2^127 sets IFQ_DEV_NONFINITE and makes that row NaN.
  *                    One pass over the cache for every 8 rows of (new token, query head)
  *                    of a key/value head.  A table with room for many more positions than
  *                    a few thousand costs short sequences some microseconds.

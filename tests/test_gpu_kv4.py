@@ -740,3 +740,18 @@ def test_attention_of_two_caches_at_once():
         torch.cuda.synchronize()
         for c in (a, b):
             assert all(torch.equal(x, y) for x, y in zip(c.alone, c.o))
+
+
+@pytest.mark.parametrize("scale,ok", [(2.0 ** 127, True), (-2.0 ** 127, True), (1.25 * 2.0 ** 127, False), (-3e38, False)])
+def test_attention_largest_scale(scale, ok):
+    """|scale| of 2^127 is taken, more counts as not finite (scale log2 e may pass float32)."""
+    c = Case([50], [2], 1, 64, 16, seed=61)
+    c.fill_random()
+    st = status_word()
+    c.attention(1, scale=scale, q_scale=2.0 ** -126, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == (0 if ok else Q.IFQ_DEV_NONFINITE)
+    if ok:
+        c.check(1)
+    else:
+        assert all(torch.isnan(x[:2]).all() for x in c.o)
