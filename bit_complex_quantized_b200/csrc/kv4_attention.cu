@@ -513,7 +513,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DIM, NT))
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           f[pl] = 1.0f;
           if (mx > cap[pl]) {
-            const int e = min(max((__float_as_int(mx) >> 23) - 127 + 2, -100), 126);  // mx < 2^(e - 1): room to grow
+            // mx < 2^(e - 1): room to grow.  From 2^-118 up, so that to_w is a float32: a weight is then off by 2^-34
+            // of cap or, for smaller scales, 2^-152, which is nothing next to float32's own last step
+            const int e = min(max((__float_as_int(mx) >> 23) - 127 + 2, -118), 126);
             f[pl] = cap[pl] * pow2(-e);
             cap[pl] = pow2(e);
             to_w[pl] = pow2(15 - kSlack - e);

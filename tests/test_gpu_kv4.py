@@ -755,3 +755,27 @@ def test_attention_largest_scale(scale, ok):
         c.check(1)
     else:
         assert all(torch.isnan(x[:2]).all() for x in c.o)
+
+
+@pytest.mark.parametrize("shared,power", [(1, -110), (1, -121), (8, -121), (2, -124)])
+def test_attention_smallest_values(shared, power):
+    """Values whose scales lie near the end of float32's range keep the stated bound (no slack but bf16's own: half a
+    step of its subnormal numbers is 2^-134)."""
+    c = Case([300, 40], [1, 1], 2, 64, 16, seed=62)
+    c.fill_random()
+    par = c.records[..., 32 * 64 + 128:]
+    bits = np.ascontiguousarray(par).view(np.uint16)
+    par[:] = F.bf16_bits(F.bf16_value(bits) * np.float32(2.0 ** power)).view(np.uint8)
+    c.d_records.copy_(to_dev(c.records))
+    c.attention(shared)
+    torch.cuda.synchronize()
+    got = torch.stack(c.o).double().cpu().numpy()
+    for b, length in enumerate(c.lens):
+        for h in range(2):
+            k, v = c.head(b, h)
+            for a in range(h * shared, (h + 1) * shared):
+                cut = slice(a * 64, (a + 1) * 64)
+                q = np.concatenate([x[b, cut] for x in c.q])[None].astype(np.float64)
+                o, bound = F.kv4_attention(q, k, v, length - 1, c.scale)
+                lim = bound[0] + 2.0 ** -8 * (np.abs(o[0]) + bound[0]) + 2.0 ** -134
+                assert np.all(np.abs(np.concatenate(got[:, b, cut]) - o[0]) <= lim), (b, a)
