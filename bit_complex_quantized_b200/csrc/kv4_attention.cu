@@ -22,8 +22,8 @@
 // Work split.  A pair is a key/value head and a tile of 4 or 8 query rows of a sequence; its work is its
 // units of 32 keys.  The four warps of a CTA share a run of units and join their parts in shared memory.
 //   few units   a cluster of up to 8 CTAs per pair, joined through distributed shared memory: one launch (777 tokens
-//               of 32 heads 6.6 us; 9 sequences of up to 3001 tokens, 5 heads, 4 new tokens 10.9 us, against
-//               14.5 us by the other form)
+//               of 32 heads 6.4 us, against 11.4 us by the other form; 9 sequences of up to 3001 tokens, 5 heads,
+//               4 new tokens 10.6 us against 13.7)
 //   otherwise   one CTA per place on the GPU, each with an equal run of the units of all pairs in a row (counted
 //               on the device, where the lengths are): a CTA ends one pair, does whole ones, begins another; the
 //               pairs that a CTA's end cuts are joined by a second, small kernel.  However ragged the
@@ -35,7 +35,7 @@
 // another pass each 8 (8 sequences of 20000 tokens, 8 heads, 8 query heads each: 1 new token 47 us, 4 148 us, 16 542 us).
 //
 // The form is chosen on the host by the positions that the page table has room for, not by the lengths, which are on the
-// device: 777 tokens of 32 heads in a table of 131072 positions take the counted form, 11.4 us instead of 6.4.
+// device: 777 tokens of 32 heads in a table of 131072 positions take the counted form.
 //
 // Rounding: the weights enter the second product as one fp16 term.  The output is bf16, whose rounding is 8 times
 // coarser; with a second term the error against 64 bits goes from 1.73 to 1.72 10^-3 (131072 tokens) and the time from 50.0
